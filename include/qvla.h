@@ -97,6 +97,8 @@ typedef enum { QVLA_SCALE_DYNAMIC = 0, QVLA_SCALE_TABLE = 1 } qvla_scale_mode;
 #define QVLA_DEVERR_STEP_RANGE 0x1u   /* device step index outside [0, T)    */
 #define QVLA_DEVERR_TIMEOUT 0x2u      /* a bounded wait in a kernel expired  */
 #define QVLA_DEVERR_TMEM 0x4u         /* tensor-memory allocation failed     */
+#define QVLA_DEVERR_CACHE_RANGE 0x8u  /* position, slot, page or length      */
+                                      /* outside its table or cache          */
 
 /* One packed linear: what qvla_pack_weights() produces.  All pointers are
  * device pointers owned by the caller.                                     */
@@ -488,6 +490,155 @@ qvla_status qvla_w4a4_gemm_batched(const qvla_linear_problem* probs, int n, int 
 qvla_status qvla_rotate_quant_act_a8_batched(const qvla_linear_problem* probs, int n,
                                              cudaStream_t stream);
 qvla_status qvla_w8a8_gemm_batched(const qvla_linear_problem* probs, int n, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * W4A16: 4-bit weights with one scale per group of inputs, activations kept
+ * in 16 or 32 bits ("Omega-QVLA: Nen VLA W4A4 tren Edge", the layers kept out
+ * of W4A4 -- state_proj, action_in / action_out_proj, time_mlp collapse under
+ * 4-bit activations -- and its W4A16 baselines).  No rotation.
+ *
+ *   y[m,n] = sum_g s[n,g] * ( sum_{k in g} (u[n,k] - z[n,g]) x[m,k] ) + b[n]
+ *
+ * group  32, 64, 128 or 256 inputs share a scale; K % group == 0,
+ *        K <= QVLA_MAX_K; N any positive size up to 2^22.
+ * wq     as in qvla_packed_linear.  w_zero NULL: two's complement codes and
+ *        z = 0.  w_zero given: unsigned codes u in [0, 15] and zero points z
+ *        in [0, 15] (only the low four bits of each byte are read).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t N, K, group;
+  int32_t sdt;              /* qvla_dtype of w_scale                         */
+  const uint8_t* wq;        /* [N][K/2] packed codes                         */
+  const void* w_scale;      /* [N][K/group] of sdt                           */
+  const uint8_t* w_zero;    /* [N][K/group] or NULL (symmetric)              */
+  const float* bias;        /* [N] or NULL                                   */
+} qvla_group_linear;
+
+/* Round-to-nearest pack of W (device fp32 [N][K], finite) into such a linear.
+ * w_zero_out NULL (symmetric): s = max|W| / 7 over the group, rounded to sdt;
+ *   code = clamp(rint(W / s), -7, 7).
+ * w_zero_out given: lo = min(W, 0), hi = max(W, 0) over the group, s = (hi -
+ *   lo) / 15 rounded to sdt, z = clamp(rint(-lo / s), 0, 15), code =
+ *   clamp(rint(W / s) + z, 0, 15).
+ * Divisions are IEEE fp32 by the rounded scale, ties to even; s = 0 gives
+ * codes and zero points 0.  Outputs (device): wq_out [N][K/2], w_scale_out
+ * [N][K/group] of sdt, w_zero_out [N][K/group].  Asynchronous.              */
+qvla_status qvla_pack_weights_w4g(const float* W, int N, int K, int group, qvla_dtype sdt,
+                                  uint8_t* wq_out, void* w_scale_out, uint8_t* w_zero_out,
+                                  cudaStream_t stream);
+
+/* y = x W^T + b for few rows of x.  x device [M][ldx] of xdt, y device
+ * [M][ldy] of ydt (ldx >= K, ldy >= N).  Every product is exact and sums are
+ * fp32 (fp32 activations enter whole); y is rounded once.  M up to 2^20:
+ * the weights are read again for every 32 rows, so many rows belong to
+ * qvla_w4a4_gemm().  The result does not depend on M or on the other rows.
+ * Asynchronous, one launch, no workspace.                                   */
+qvla_status qvla_w4a16_gemv(const void* x, qvla_dtype xdt, int M, int ldx,
+                            const qvla_group_linear* L, void* y, qvla_dtype ydt, int ldy,
+                            cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged key/value cache of the attention between two linears.  Slot t of the
+ * cache is token t % page_size of page t / page_size.  k and v share the
+ * strides (in elements), which give any order of page, token and head:
+ *   value d of head h of a slot: [page * page_stride + token * token_stride
+ *                                 + h * head_stride + d].
+ * bits 16: bf16 values.  bits 8: int8 codes with one fp32 scale per (slot,
+ * head) at [page * s_page_stride + token * s_token_stride + h * s_head_stride]
+ * of k_scale / v_scale; value = scale * code.
+ * dim: a multiple of 16 up to 256.  pages * page_size < 2^31.  k, v and every
+ * stride (in bytes) 16-byte aligned; scales 4-byte aligned.  The strides of
+ * extents above 1 are at least dim.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t pages, page_size, heads, dim;
+  int32_t bits;
+  void* k;                  /* device                                        */
+  void* v;                  /* device                                        */
+  int64_t page_stride, token_stride, head_stride;
+  float* k_scale;           /* device, bits == 8                             */
+  float* v_scale;           /* device, bits == 8                             */
+  int64_t s_page_stride, s_token_stride, s_head_stride;
+} qvla_kv_cache;
+
+/* Cosines and sines of p * inv_freq[i] for positions p in [0, P): row p of
+ * table (device fp32 [P][2 * half]) holds half cosines, then half sines.  The
+ * angle and its cosine and sine are formed in fp64 and rounded once, so far
+ * positions are as exact as near ones.  inv_freq host fp64 [half], half in
+ * [1, 128], read before the call returns.  Asynchronous.                    */
+qvla_status qvla_rope_table(const double* inv_freq, int half, int P, float* table,
+                            cudaStream_t stream);
+
+/* RMS norm of every query and key head and their position rotation in one
+ * pass over the output rows of the q, k, v linears, with the keys and values
+ * written to the paged cache:
+ *   h' = h * w / sqrt(mean(h^2) + eps)     (w NULL: h' = h, no norm)
+ *   pairs (a, b) of its first `rot` values become (a c - b s, b c + a s)
+ * with c, s the table's cosine and sine of the pair at the token's position.
+ * Pair i is (h'[i], h'[i + rot/2]), or (h'[2i], h'[2i + 1]) if interleaved.
+ * Values are norm, rotated and quantised in fp32, and rounded once.
+ *
+ * q, k, v   device rows [T][ldq], [T][ldk], [T][ldv] of xdt: Hq, Hkv, Hkv
+ *           heads of dim D one after the other (they may be parts of one
+ *           row).  q NULL if Hq == 0; k and v NULL if Hkv == 0; v may be NULL
+ *           when there is no cache.  D a multiple of 16 up to 256.
+ * q_norm, k_norm  device fp32 [D] or NULL.
+ * rope_table      device fp32 [P][rot], rot a multiple of 16 up to D, or NULL
+ *           (no rotation; positions and rot are ignored).
+ * positions device int32 [T].  A position outside [0, P) sets
+ *           QVLA_DEVERR_CACHE_RANGE: that token's q_out and k_out rows become
+ *           0 and its slot is left as it was.
+ * cache, slots    NULL, or the cache (heads == Hkv, dim == D) and the slot of
+ *           each token (device int32 [T]).  A negative slot writes nothing
+ *           (padding); one past the cache sets QVLA_DEVERR_CACHE_RANGE and
+ *           writes nothing.  Slots of one call must differ.  No other byte
+ *           of the cache is touched.  bits 8: per row s = max|x| / 127, code
+ *           = clamp(rint(x / s), -128, 127), as qvla_rotate_quant_act_a8().
+ * q_out, k_out    device rows of xdt [T][ldqo], [T][ldko]; may be q and k
+ *           themselves (same pitch).  k_out may be NULL.
+ * Asynchronous, one launch.                                                 */
+qvla_status qvla_qk_norm_rope(const void* q, const void* k, const void* v, qvla_dtype xdt, int T,
+                              int Hq, int Hkv, int D, int ldq, int ldk, int ldv,
+                              const float* q_norm, const float* k_norm, float eps,
+                              const float* rope_table, int P, int rot, int interleaved,
+                              const int32_t* positions, const qvla_kv_cache* cache,
+                              const int32_t* slots, void* q_out, int ldqo, void* k_out, int ldko,
+                              cudaStream_t stream);
+
+/* Attention of one new token per sequence over the paged cache:
+ *   o[b,h] = sum_t p_t v_t,  p = softmax over the visible t of
+ *            scale * q[b,h] . k_t       (key head h / (Hq / heads))
+ * q         device [B][ldq] of qdt: Hq heads of cache->dim; Hq a multiple of
+ *           cache->heads.
+ * page_table device int32 [B][max_pages]: page of tokens [i * page_size,
+ *           (i + 1) * page_size) of sequence b.  Entries past the sequence's
+ *           last page are not read.
+ * seq_lens  device int32 [B]: tokens of sequence b in the cache, the new one
+ *           among them.  0 gives o = 0 and lse = -inf.
+ * window, sinks  window 0: every token is visible.  Else the last `window`
+ *           tokens and the first `sinks` are.  Hidden tokens are not read.
+ * out       device [B][ldo] of qdt.  lse device fp32 [B][Hq] or NULL: the
+ *           natural logarithm of the sum of exponentials (to join this result
+ *           with attention over other keys).
+ * workspace device, >= qvla_paged_attn_workspace_bytes(); its contents need
+ *           not start at anything and mean nothing afterwards.  Calls (or
+ *           graphs) that may run at the same time need one each.
+ * A length outside [0, max_pages * page_size] sets QVLA_DEVERR_CACHE_RANGE
+ * and gives o = 0, lse = -inf; a page outside the cache sets it and its
+ * tokens are left out.  Cache rows that no visible token owns are not read
+ * (they may hold anything).  Products and sums are fp32; for bf16 q the
+ * probabilities enter the second product as bf16, for fp32 q whole.  The
+ * split of the work, and with it the order of the sums, depends on all
+ * lengths of the call and is the same for equal calls.
+ * Asynchronous, two launches.  B <= 2^16, B * Hq < 2^31.                    */
+qvla_status qvla_paged_attn_decode(const void* q, qvla_dtype qdt, int B, int Hq, int ldq,
+                                   const qvla_kv_cache* cache, const int32_t* page_table,
+                                   int max_pages, const int32_t* seq_lens, float scale,
+                                   int window, int sinks, void* out, int ldo, float* lse,
+                                   void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Scratch of qvla_paged_attn_decode(), whatever B and the lengths are.       */
+qvla_status qvla_paged_attn_workspace_bytes(int Hq, int heads, int dim, size_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,216 @@
+"""W4A16 products with group scales on the GPU against fp64."""
+import pytest
+import torch
+
+import _decode_ref as R
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def q():
+    from w4a4_post_quantization_zigzag_b200 import build
+    build.build()
+    from w4a4_post_quantization_zigzag_b200 import qvla
+    assert torch.cuda.is_available()
+    return qvla
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def weights(N, K, G, sdt=F32, zero=False, seed=0):
+    g = gen(seed)
+    wq = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = (0.01 + 0.05 * torch.rand(N, K // G, device="cuda", generator=g)).to(sdt)
+    z = torch.randint(0, 16, (N, K // G), dtype=torch.uint8, device="cuda", generator=g) if zero else None
+    return wq, s, z
+
+
+def rows(M, K, dt, seed=1):
+    return torch.randn(M, K, device="cuda", generator=gen(seed)).to(dt)
+
+
+def check(q, x, wq, s, z=None, bias=None, ydt=None, **kw):
+    y = q.qvla_w4a16_gemv(x, wq, s, z, bias, out_dtype=ydt, **kw)
+    ref, slack = R.gemv(x, wq, s, z, bias)
+    R.within(y, ref, slack, f"x {tuple(x.shape)} w {tuple(wq.shape)} groups {tuple(s.shape)}")
+    return y
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16])
+@pytest.mark.parametrize("xdt,ydt,sdt,zero", [(BF, BF, F32, False), (BF, F32, BF, True),
+                                              (F32, F32, F32, True), (F32, BF, BF, False)])
+def test_types_groups_and_batches(q, group, M, xdt, ydt, sdt, zero):
+    N, K = 200, group * 5
+    wq, s, z = weights(N, K, group, sdt, zero, seed=group + M)
+    bias = torch.randn(N, device="cuda", generator=gen(3))
+    check(q, rows(M, K, xdt), wq, s, z, bias, ydt)
+
+
+@pytest.mark.parametrize("N", [1, 3, 8, 15, 16, 17, 31, 33, 127, 1000, 4096])
+@pytest.mark.parametrize("K", [32, 96, 128, 160, 1024, 2080])
+def test_odd_sizes(q, N, K):
+    wq, s, z = weights(N, K, 32, seed=N + K)
+    check(q, rows(1, K, BF), wq, s)
+    check(q, rows(5, K, F32), wq, s)
+
+
+@pytest.mark.parametrize("M", [17, 31, 32, 33, 64, 100])
+def test_many_rows(q, M):
+    wq, s, z = weights(130, 512, 128, zero=True)
+    check(q, rows(M, 512, BF), wq, s, z)
+    check(q, rows(M, 512, F32), wq, s, z)
+
+
+@pytest.mark.parametrize("N,K,group,M", [(64, 16384, 128, 1), (2048, 16384, 128, 3),
+                                         (16384, 2048, 64, 1), (40, 32768, 256, 16),
+                                         (70000, 256, 32, 2)])
+def test_long_and_wide(q, N, K, group, M):
+    wq, s, z = weights(N, K, group, BF, True)
+    check(q, rows(M, K, BF), wq, s, z)
+
+
+def test_offsets_past_32_bits(q):
+    """Codes of 4.3 GB: the last rows lie past 2^32 bytes."""
+    N, K = 262144 + 40, 32768
+    wq = torch.empty(N, K // 2, dtype=torch.uint8, device="cuda")
+    wq.random_(0, 256, generator=gen(5))
+    s = 0.01 + 0.05 * torch.rand(N, K // 256, device="cuda", generator=gen(6))
+    x = rows(1, K, BF)
+    y = q.qvla_w4a16_gemv(x, wq, s, out_dtype=F32)
+    for part in (slice(0, 64), slice(N - 64, N)):
+        ref, slack = R.gemv(x, wq[part], s[part])
+        R.within(y[:, part], ref, slack, "rows at the ends")
+
+
+def test_one_input_at_a_time_is_exact(q):
+    """A row with a single nonzero input is one exact product, one scaling: fp32 activations
+    enter whole (all 24 bits), at every place of K."""
+    N, K, G = 32, 512, 64
+    wq, s, z = weights(N, K, G, zero=True)
+    k = torch.arange(K, device="cuda")
+    for m0 in range(0, K, 16):
+        x = torch.zeros(16, K, device="cuda")
+        x[torch.arange(16), k[m0:m0 + 16]] = 1.0 + torch.rand(16, device="cuda", generator=gen(m0)) \
+            + 2.0 ** -23
+        y = q.qvla_w4a16_gemv(x, wq, s, z)
+        ref, _ = R.gemv(x, wq, s, z)
+        # the product of 24 and 4 bits may round once, the scaling once, both sums are with zeros
+        R.within(y, ref, 2 * R.U * ref.abs(), f"k {m0}..")
+
+
+def test_extreme_activations(q):
+    """The largest finite fp32 values and values below bf16's normal range; an infinite or NaN
+    row leaves the others alone."""
+    N, K, G = 48, 256, 64
+    wq, s, _ = weights(N, K, G)
+    wq = wq & 0x11                             # codes 0 and 1: sums of few large values
+    for big in (3.0e38, 1e-37, 1e-38):
+        x = torch.zeros(3, K, device="cuda")
+        x[:, 5] = big * torch.tensor([1.0, 0.77, 0.123456789], device="cuda")
+        y = q.qvla_w4a16_gemv(x, wq, s)
+        ref, _ = R.gemv(x, wq, s)
+        R.within(y, ref, 2 * R.U * ref.abs() + 2.0 ** -126 * 2 ** -8, f"value {big}")
+    x = rows(5, K, F32)
+    clean = q.qvla_w4a16_gemv(x, wq, s)
+    x[1, 7], x[3, 9] = float("inf"), float("nan")
+    y = q.qvla_w4a16_gemv(x, wq, s)
+    assert torch.equal(y[[0, 2, 4]], clean[[0, 2, 4]])
+    assert y[3].isnan().all() and not y[1].isfinite().any()
+
+
+def test_rows_do_not_depend_on_the_batch(q):
+    wq, s, z = weights(300, 1024, 128, zero=True)
+    for dt in (BF, F32):
+        x = rows(40, 1024, dt)
+        whole = q.qvla_w4a16_gemv(x, wq, s, z, out_dtype=F32)
+        for M in (1, 8, 9, 17):
+            assert torch.equal(q.qvla_w4a16_gemv(x[:M], wq, s, z, out_dtype=F32), whole[:M])
+
+
+def test_pitches_and_given_output(q):
+    """Rows inside wider buffers; what lies outside the output rows stays."""
+    N, K = 72, 256
+    wq, s, _ = weights(N, K, 64)
+    xb = rows(6, 512, BF)
+    for ydt in (BF, F32):
+        buf = torch.full((6, 128), 7.0, dtype=ydt, device="cuda")
+        y = q.qvla_w4a16_gemv(xb[:, 128:384], wq, s, y=buf[:, 16:16 + N])
+        ref, slack = R.gemv(xb[:, 128:384], wq, s)
+        R.within(y, ref, slack)
+        assert (buf[:, :16] == 7).all() and (buf[:, 16 + N:] == 7).all()
+
+
+def test_zero_points_use_their_low_bits(q):
+    wq, s, z = weights(40, 128, 32, zero=True)
+    x = rows(2, 128, BF)
+    assert torch.equal(q.qvla_w4a16_gemv(x, wq, s, z), q.qvla_w4a16_gemv(x, wq, s, z + 32))
+
+
+def test_nothing_to_do(q):
+    wq, s, _ = weights(40, 128, 32)
+    assert q.qvla_w4a16_gemv(rows(0, 128, BF), wq, s).shape == (0, 40)
+
+
+def test_graph_and_side_stream(q):
+    wq, s, z = weights(500, 1024, 128, zero=True)
+    x = rows(3, 1024, BF)
+    y = torch.empty(3, 500 + 4, dtype=BF, device="cuda")[:, :500]
+    want = q.qvla_w4a16_gemv(x, wq, s, z)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        q.qvla_w4a16_gemv(x, wq, s, z, y=y)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            q.qvla_w4a16_gemv(x, wq, s, z, y=y)
+    torch.cuda.synchronize()
+    x2 = rows(3, 1024, BF, seed=9)
+    x.copy_(x2)
+    y.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, q.qvla_w4a16_gemv(x2, wq, s, z))
+    assert not torch.equal(y, want)
+    other = q.qvla_w4a16_gemv(x2, wq, s, z, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(other, y)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("sdt", [F32, BF])
+@pytest.mark.parametrize("zero", [False, True])
+def test_pack(q, group, sdt, zero):
+    """Codes, scales and zero points by the stated rule (the same IEEE fp32 operations in torch),
+    and the packed product near the original one."""
+    N, K = 50, 2 * 256
+    W = torch.randn(N, K, device="cuda", generator=gen(group)) * 0.02
+    W[0] = 0
+    W[1, :group] = W[1, :group].abs()
+    W[2, :group] = -W[2, :group].abs()
+    wq, s, z = q.qvla_pack_weights_w4g(W, group, zero, sdt)
+    w = W.view(N, K // group, group)
+    seven, fifteen = (torch.full((), v, device="cuda") for v in (7.0, 15.0))   # tensors: a true division
+    if zero:
+        lo, hi = w.amin(2).clamp(max=0), w.amax(2).clamp(min=0)
+        want_s = ((hi - lo) / fifteen).to(sdt)
+        sf = want_s.float()
+        want_z = torch.where(sf > 0, torch.round(-lo / sf).clamp(0, 15), 0.0)
+        c = torch.where(sf[..., None] > 0, (torch.round(w / sf[..., None]) + want_z[..., None]).clamp(0, 15), 0.0)
+        assert torch.equal(z, want_z.to(torch.uint8))
+        err = (c - want_z[..., None]) * sf[..., None] - w
+    else:
+        want_s = (w.abs().amax(2) / seven).to(sdt)
+        sf = want_s.float()
+        c = torch.where(sf[..., None] > 0, torch.round(w / sf[..., None]).clamp(-7, 7), 0.0)
+        assert z is None
+        err = c * sf[..., None] - w
+    assert torch.equal(s, want_s)
+    assert torch.equal(R.unpack(wq, not zero), c.view(N, K).double())
+    # rounding to a step, the ends may miss by the rounding of the scale
+    assert (err.abs() <= sf[..., None] * (0.5 + 15 * R.half_step(sdt) + (1.0 if zero else 0) * 0.5 + 1e-5)).all()
+    check(q, rows(2, K, BF), wq, s, z)

@@ -128,4 +128,65 @@ cudaError_t launch_w8a8_gemm(const GemmArgs& g, cudaStream_t stream);
 // independent W8A8 linears, grouped by token tile, up to 16 per launch
 cudaError_t launch_w8a8_gemm_batch(const GemmArgs* gs, int n, cudaStream_t stream);
 
+// ---- W4A16 with group scales (gemv_w4a16.cu)
+cudaError_t launch_pack_w4g(const float* W, int N, int K, int group, qvla_dtype sdt, uint8_t* wq,
+                            void* scale, uint8_t* zero, cudaStream_t s);
+struct GemvArgs {
+  const void* x;
+  qvla_dtype xdt;
+  int M, ldx, N, K, group;
+  qvla_dtype sdt;
+  const uint8_t* wq;
+  const void* scale;
+  const uint8_t* zero;    // or nullptr: two's complement codes
+  const float* bias;      // or nullptr
+  void* y;
+  qvla_dtype ydt;
+  int ldy;
+};
+cudaError_t launch_w4a16_gemv(const GemvArgs& a, cudaStream_t stream);
+
+// ---- norm + rotation of query and key heads, cache write (qk_norm_rope.cu)
+struct RopeFreqs {
+  double f[128];
+};
+cudaError_t launch_rope_table(const RopeFreqs& freqs, int half, int P, float* table,
+                              cudaStream_t s);
+struct NormRopeArgs {
+  const void *q, *k, *v;
+  qvla_dtype xdt;
+  int T, Hq, Hkv, D;
+  int64_t ldq, ldk, ldv;
+  const float *q_norm, *k_norm;
+  float eps;
+  const float* table;     // [P][rot] or nullptr
+  int P, rot, interleaved;
+  const int32_t *positions, *slots;
+  int has_cache;
+  qvla_kv_cache cache;
+  void *q_out, *k_out;    // k_out may be nullptr
+  int64_t ldqo, ldko;
+};
+cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+
+// ---- attention of one new token over the paged cache (paged_attn.cu)
+struct PagedAttnArgs {
+  const void* q;
+  qvla_dtype qdt;
+  int B, Hq;
+  int64_t ldq;
+  qvla_kv_cache cache;
+  const int32_t* page_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  float scale;
+  int window, sinks;
+  void* out;
+  int64_t ldo;
+  float* lse;
+  void* ws;
+};
+size_t paged_attn_ws_bytes(int Hq, int heads, int dim);
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
+
 }  // namespace qvla

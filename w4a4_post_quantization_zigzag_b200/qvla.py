@@ -10,7 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_double, c_int, c_int32, c_size_t, c_uint32, c_void_p
+from ctypes import (POINTER, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32,
+                    c_void_p)
 from typing import Optional, Tuple
 
 import numpy as np
@@ -57,6 +58,7 @@ QVLA_SCALE_TABLE = 1
 QVLA_DEVERR_STEP_RANGE = 0x1
 QVLA_DEVERR_TIMEOUT = 0x2
 QVLA_DEVERR_TMEM = 0x4
+QVLA_DEVERR_CACHE_RANGE = 0x8
 
 # Every symbol include/qvla.h declares.
 EXPORTED = (
@@ -69,7 +71,8 @@ EXPORTED = (
     "qvla_rotate_quant_a8_workspace_bytes", "qvla_w8a8_gemm", "qvla_w8a8_gemm_s32",
     "qvla_gptq_quantize_host", "qvla_pack_weights_gptq", "qvla_gptq_hessian_host",
     "qvla_selftest_wait_timeout", "qvla_source_hash", "qvla_rotate_quant_act_a8_batched",
-    "qvla_w8a8_gemm_batched",
+    "qvla_w8a8_gemm_batched", "qvla_pack_weights_w4g", "qvla_w4a16_gemv", "qvla_rope_table",
+    "qvla_qk_norm_rope", "qvla_paged_attn_decode", "qvla_paged_attn_workspace_bytes",
 )
 
 QVLA_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -88,6 +91,19 @@ class qvla_linear_problem(ctypes.Structure):
                 ("step_host", c_int32), ("layer", c_int32), ("xq", c_void_p), ("s_x", c_void_p),
                 ("y", c_void_p), ("ldy", c_int32), ("workspace", c_void_p),
                 ("ws_bytes", c_size_t), ("xq8", c_void_p)]
+
+
+class qvla_group_linear(ctypes.Structure):
+    _fields_ = [("N", c_int32), ("K", c_int32), ("group", c_int32), ("sdt", c_int32),
+                ("wq", c_void_p), ("w_scale", c_void_p), ("w_zero", c_void_p), ("bias", c_void_p)]
+
+
+class qvla_kv_cache(ctypes.Structure):
+    _fields_ = [("pages", c_int32), ("page_size", c_int32), ("heads", c_int32), ("dim", c_int32),
+                ("bits", c_int32), ("k", c_void_p), ("v", c_void_p), ("page_stride", c_int64),
+                ("token_stride", c_int64), ("head_stride", c_int64), ("k_scale", c_void_p),
+                ("v_scale", c_void_p), ("s_page_stride", c_int64), ("s_token_stride", c_int64),
+                ("s_head_stride", c_int64)]
 
 
 _P = POINTER(qvla_packed_linear)
@@ -141,6 +157,20 @@ _sig = {
     "qvla_w4a4_gemm_batched": (c_int, [_PP, c_int, c_int, c_void_p]),
     "qvla_rotate_quant_act_a8_batched": (c_int, [_PP, c_int, c_void_p]),
     "qvla_w8a8_gemm_batched": (c_int, [_PP, c_int, c_void_p]),
+    "qvla_pack_weights_w4g": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
+                                      c_void_p, c_void_p]),
+    "qvla_w4a16_gemv": (c_int, [c_void_p, c_int, c_int, c_int, POINTER(qvla_group_linear),
+                                c_void_p, c_int, c_int, c_void_p]),
+    "qvla_rope_table": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p]),
+    "qvla_qk_norm_rope": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                  c_int, c_int, c_int, c_void_p, c_void_p, c_float, c_void_p,
+                                  c_int, c_int, c_int, c_void_p, POINTER(qvla_kv_cache), c_void_p,
+                                  c_void_p, c_int, c_void_p, c_int, c_void_p]),
+    "qvla_paged_attn_decode": (c_int, [c_void_p, c_int, c_int, c_int, c_int,
+                                       POINTER(qvla_kv_cache), c_void_p, c_int, c_void_p, c_float,
+                                       c_int, c_int, c_void_p, c_int, c_void_p, c_void_p, c_size_t,
+                                       c_void_p]),
+    "qvla_paged_attn_workspace_bytes": (c_int, [c_int, c_int, c_int, POINTER(c_size_t)]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -676,3 +706,268 @@ def qvla_w8a8_gemm_batched(problems, stream=None):
     arr = _problem_array(problems)
     _check(_lib.qvla_w8a8_gemm_batched(arr, len(problems), _stream(stream)),
            "qvla_w8a8_gemm_batched")
+
+
+# --------------------------------------------------------------------------
+# Operators around the linears of a decode step
+# --------------------------------------------------------------------------
+
+def _launch(fn, where: str, device: int, stream, *args):
+    """fn(*args, stream) with `device` current; by default on its current stream."""
+    if device < 0:
+        raise ValueError(f"{where}: the tensors must be on a CUDA device")
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(fn, where, device, stream, *args)
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        st = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    rc = fn(*args, st)
+    if rc != QVLA_OK:
+        raise QvlaError(rc, where)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output or scratch tensor whose memory belongs to the stream the
+    kernel runs on, so that its earlier and later uses there are in order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _expect_on(t: torch.Tensor, dtype, shape, device: int, name: str):
+    """A dense tensor of exactly this type and shape on CUDA device `device`."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != device
+            or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on cuda:{device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+
+
+def qvla_pack_weights_w4g(W: torch.Tensor, group: int = 128, zero_points: bool = False,
+                          scale_dtype=torch.float32, stream=None):
+    """4-bit codes of W (cuda fp32 [N, K]) with one scale per `group` inputs:
+    (wq uint8 [N, K/2], w_scale [N, K/group], w_zero uint8 [N, K/group] or None)."""
+    if W.dim() != 2:
+        raise ValueError(f"W: expected [N, K], got shape {tuple(W.shape)}")
+    N, K = W.shape
+    dev = W.get_device()
+    _expect_on(W, torch.float32, (N, K), dev, "W")
+    if group <= 0 or K % group:
+        raise QvlaError(QVLA_ERR_SHAPE, "qvla_pack_weights_w4g")
+    wq = _empty((N, K // 2), torch.uint8, W.device, stream)
+    scale = _empty((N, K // group), scale_dtype, W.device, stream)
+    zero = _empty((N, K // group), torch.uint8, W.device, stream) if zero_points else None
+    _launch(_lib.qvla_pack_weights_w4g, "qvla_pack_weights_w4g", dev, stream, W.data_ptr(), N, K,
+            group, _dtype_code(scale), wq.data_ptr(), scale.data_ptr(),
+            None if zero is None else zero.data_ptr())
+    return wq, scale, zero
+
+
+def qvla_w4a16_gemv(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
+                    w_zero: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                    y: Optional[torch.Tensor] = None, out_dtype=None,
+                    stream=None) -> torch.Tensor:
+    """y [M, N] = x W^T + bias for few rows x (bf16 or fp32 [M, K]) and the
+    group-quantised weights of qvla_pack_weights_w4g(); y has out_dtype
+    (default: x's)."""
+    N, Kh = wq.shape
+    K, groups = 2 * Kh, w_scale.shape[-1]
+    dev = x.get_device()
+    _expect_rows(x, K)
+    _expect_on(wq, torch.uint8, (N, Kh), dev, "wq")
+    _expect_on(w_scale, w_scale.dtype, (N, groups), dev, "w_scale")
+    if groups == 0 or K % groups:
+        raise ValueError(f"w_scale: {groups} groups do not divide {K} inputs")
+    if w_zero is not None:
+        _expect_on(w_zero, torch.uint8, (N, groups), dev, "w_zero")
+    if bias is not None:
+        _expect_on(bias, torch.float32, (N,), dev, "bias")
+    M = x.shape[0]
+    if y is None:
+        # rows whose pitch is a multiple of 16 bytes
+        dt = out_dtype or x.dtype
+        y = _empty((M, (N + 7) // 8 * 8), dt, x.device, stream)
+        if N % 8:
+            y = y[:, :N]
+    elif (tuple(y.shape) != (M, N) or y.get_device() != dev or (y.numel() and y.stride(1) != 1)
+          or (out_dtype is not None and y.dtype != out_dtype)):
+        raise ValueError(f"y: expected [{M}, {N}] rows with unit stride on {x.device}")
+    L = qvla_group_linear(N, K, K // groups, _dtype_code(w_scale), wq.data_ptr(),
+                          w_scale.data_ptr(), None if w_zero is None else w_zero.data_ptr(),
+                          None if bias is None else bias.data_ptr())
+    _launch(_lib.qvla_w4a16_gemv, "qvla_w4a16_gemv", dev, stream, x.data_ptr(), _dtype_code(x), M,
+            x.stride(0) if M > 1 else K, L, y.data_ptr(), _dtype_code(y),
+            y.stride(0) if M > 1 else (N + 7) // 8 * 8)
+    return y
+
+
+def qvla_rope_table(inv_freq, P: int, device="cuda", stream=None) -> torch.Tensor:
+    """fp32 [P, 2 * len(inv_freq)]: cosines, then sines, of p * inv_freq for
+    positions p < P (inv_freq: host float64, one entry per pair)."""
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if f.ndim != 1:
+        raise ValueError("inv_freq: expected one frequency per pair")
+    table = _empty((P, 2 * f.shape[0]), torch.float32, torch.device(device), stream)
+    _launch(_lib.qvla_rope_table, "qvla_rope_table", table.get_device(), stream,
+            f.ctypes.data_as(c_void_p), f.shape[0], P, table.data_ptr())
+    return table
+
+
+def _head_rows(x: torch.Tensor, device: int, dtype, name: str):
+    """[rows, heads, dim] with heads one after the other (any row pitch)."""
+    if x.dim() != 3 or x.dtype is not dtype or x.get_device() != device:
+        raise ValueError(f"{name}: expected a [rows, heads, dim] {dtype} tensor on cuda:{device}, "
+                         f"got {x.dtype} {tuple(x.shape)} on {x.device}")
+    T, H, D = x.shape
+    st = x.stride()
+    if x.numel() and ((D > 1 and st[2] != 1) or (H > 1 and st[1] != D)):
+        raise ValueError(f"{name}: the heads of a row must lie one after the other, "
+                         f"got strides {tuple(st)}")
+    return st[0] if T > 1 else H * D
+
+
+def _kv_struct(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale, device: int):
+    """The C cache of [pages, page_size, heads, dim] views in any memory order
+    (bf16, or int8 with fp32 scales [pages, page_size, heads])."""
+    shape, st, dt = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if k_cache.dim() != 4 or (shape[3] > 1 and st[3] != 1):
+        raise ValueError("k_cache: expected [pages, page_size, heads, dim] with unit stride "
+                         f"along dim, got shape {tuple(shape)} strides {tuple(st)}")
+    if v_cache.shape != shape or v_cache.stride() != st or v_cache.dtype is not dt:
+        raise ValueError("v_cache: expected the shape, strides and type of k_cache")
+    if k_cache.get_device() != device or v_cache.get_device() != device:
+        raise ValueError(f"k_cache, v_cache: expected them on cuda:{device}")
+    if dt is torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale, v_scale: a bf16 cache has none")
+        return qvla_kv_cache(*shape, 16, k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1],
+                             st[2], None, None, 0, 0, 0)
+    if dt is not torch.int8:
+        raise TypeError(f"unsupported cache dtype {dt}")
+    for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if (s is None or s.dtype is not torch.float32 or s.shape != shape[:3]
+                or s.get_device() != device):
+            raise ValueError(f"{name}: expected fp32 {tuple(shape[:3])} on cuda:{device}")
+    ss = k_scale.stride()
+    if v_scale.stride() != ss:
+        raise ValueError("v_scale: expected the strides of k_scale")
+    return qvla_kv_cache(*shape, 8, k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2],
+                         k_scale.data_ptr(), v_scale.data_ptr(), ss[0], ss[1], ss[2])
+
+
+def qvla_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                      v: Optional[torch.Tensor] = None, q_norm: Optional[torch.Tensor] = None,
+                      k_norm: Optional[torch.Tensor] = None,
+                      rope_table: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None,
+                      slots: Optional[torch.Tensor] = None,
+                      k_cache: Optional[torch.Tensor] = None,
+                      v_cache: Optional[torch.Tensor] = None, k_scale=None, v_scale=None,
+                      eps: float = 1e-6, interleaved: bool = False,
+                      q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                      stream=None):
+    """RMS norm of the heads of q [T, Hq, D] and k [T, Hkv, D], position
+    rotation by rope_table (qvla_rope_table()) at `positions`, and k and v
+    written to the cache slots `slots` (negative: not written).  Returns
+    q_out; without a cache (q_out, k_out).  q_out / k_out may be q / k."""
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q, k: at least one is needed")
+    T, D, dt, dev = one.shape[0], one.shape[-1], one.dtype, one.get_device()
+    ldq = ldk = ldv = ldqo = ldko = 0
+    Hq = Hkv = 0
+    if q is not None:
+        ldq, Hq = _head_rows(q, dev, dt, "q"), q.shape[1]
+        if q_out is None:
+            q_out = _empty((T, Hq, D), dt, q.device, stream)
+        ldqo = _head_rows(q_out, dev, dt, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError(f"q_out: expected shape {tuple(q.shape)}")
+    if k is not None:
+        ldk, Hkv = _head_rows(k, dev, dt, "k"), k.shape[1]
+        if k.shape != (T, Hkv, D):
+            raise ValueError(f"k: expected [{T}, heads, {D}], got {tuple(k.shape)}")
+        if k_out is None and k_cache is None:
+            k_out = _empty((T, Hkv, D), dt, k.device, stream)
+        if k_out is not None:
+            ldko = _head_rows(k_out, dev, dt, "k_out")
+            if k_out.shape != k.shape:
+                raise ValueError(f"k_out: expected shape {tuple(k.shape)}")
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _expect_on(w, torch.float32, (D,), dev, name)
+    P = rot = 0
+    if rope_table is not None:
+        P, rot = rope_table.shape
+        _expect_on(rope_table, torch.float32, (P, rot), dev, "rope_table")
+        if positions is None:
+            raise ValueError("positions: needed with rope_table")
+        _expect_on(positions, torch.int32, (T,), dev, "positions")
+    cache = None
+    if k_cache is not None:
+        if k is None or v is None or slots is None or v_cache is None:
+            raise ValueError("a cache needs k, v, slots and v_cache")
+        ldv = _head_rows(v, dev, dt, "v")
+        if v.shape != k.shape:
+            raise ValueError(f"v: expected shape {tuple(k.shape)}")
+        _expect_on(slots, torch.int32, (T,), dev, "slots")
+        cache = _kv_struct(k_cache, v_cache, k_scale, v_scale, dev)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _launch(_lib.qvla_qk_norm_rope, "qvla_qk_norm_rope", dev, stream, p(q), p(k),
+            p(v) if cache is not None else None, _dtype_code(one), T, Hq, Hkv, D, ldq, ldk, ldv,
+            p(q_norm), p(k_norm), eps, p(rope_table), P, rot, int(interleaved), p(positions),
+            cache, p(slots), p(q_out), ldqo, p(k_out), ldko)
+    return q_out if cache is not None else (q_out, k_out)
+
+
+def qvla_paged_attn_workspace_bytes(Hq: int, heads: int, dim: int) -> int:
+    b = c_size_t()
+    _check(_lib.qvla_paged_attn_workspace_bytes(Hq, heads, dim, ctypes.byref(b)),
+           "qvla_paged_attn_workspace_bytes")
+    return b.value
+
+
+def qvla_paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           page_table: torch.Tensor, seq_lens: torch.Tensor,
+                           scale: Optional[float] = None, window: int = 0, sinks: int = 0,
+                           k_scale=None, v_scale=None, out: Optional[torch.Tensor] = None,
+                           lse: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence, q [B, Hq, D], over the paged
+    cache; scale defaults to D ** -0.5.  lse: optional fp32 [B, Hq] output.
+    workspace: uint8 device scratch of qvla_paged_attn_workspace_bytes()
+    (allocated per call when None)."""
+    dt, dev = q.dtype, q.get_device()
+    ldq = _head_rows(q, dev, dt, "q")
+    B, Hq, D = q.shape
+    cache = _kv_struct(k_cache, v_cache, k_scale, v_scale, dev)
+    if cache.dim != D:
+        raise ValueError(f"k_cache: expected dim {D}, got {cache.dim}")
+    _expect_on(seq_lens, torch.int32, (B,), dev, "seq_lens")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected [{B}, pages], got {tuple(page_table.shape)}")
+    max_pages = page_table.shape[1]
+    _expect_on(page_table, torch.int32, (B, max_pages), dev, "page_table")
+    if out is None:
+        out = _empty((B, Hq, D), dt, q.device, stream)
+    elif out.shape != q.shape:
+        raise ValueError(f"out: expected shape {tuple(q.shape)}")
+    ldo = _head_rows(out, dev, dt, "out")
+    if lse is not None:
+        _expect_on(lse, torch.float32, (B, Hq), dev, "lse")
+    if workspace is None:
+        workspace = _empty(qvla_paged_attn_workspace_bytes(Hq, cache.heads, D), torch.uint8,
+                           q.device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous memory on cuda:{dev}")
+    _launch(_lib.qvla_paged_attn_decode, "qvla_paged_attn_decode", dev, stream, q.data_ptr(),
+            _dtype_code(q), B, Hq, ldq, cache, page_table.data_ptr(), max_pages,
+            seq_lens.data_ptr(), D ** -0.5 if scale is None else scale, window, sinks,
+            out.data_ptr(), ldo, None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return out
