@@ -16,9 +16,11 @@ def within(out, ref, slack, what=""):
     lim = slack + half_step(out.dtype) * (ref.abs() + slack)
     if out.dtype == torch.bfloat16:
         lim = lim + 2.0 ** -134            # half of the smallest subnormal step
-    bad = ~((out.double() - ref).abs() <= lim)
+    err = (out.double() - ref).abs()
+    bad = ~(err <= lim)
     assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} values outside, worst "
-                           f"{((out.double() - ref).abs() / lim).nan_to_num(9e9).max():.3g} x the bound")
+                           f"{(err / lim)[bad].max():.4g} x the bound, at {bad.nonzero()[0].tolist()}: "
+                           f"{out[bad][0].item()!r} for {ref[bad][0].item()!r}")
 
 
 def unpack(wq, signed):
