@@ -66,12 +66,14 @@ def test_many_rows(q, M):
     check(q, rows(M, 512, F32), wq, s, z)
 
 
-@pytest.mark.parametrize("N,K,group,M", [(64, 16384, 128, 1), (2048, 16384, 128, 3),
+@pytest.mark.parametrize("N,K,group,M", [(64, 16384, 128, 1), (100, 32768, 32, 2), (8200, 32768, 32, 1),
+                                         (8200, 32768, 32, 3), (20000, 8192, 64, 2), (9000, 4096, 128, 9), (2048, 16384, 128, 3),
                                          (16384, 2048, 64, 1), (40, 32768, 256, 16),
                                          (70000, 256, 32, 2)])
 def test_long_and_wide(q, N, K, group, M):
     wq, s, z = weights(N, K, group, BF, True)
     check(q, rows(M, K, BF), wq, s, z)
+    check(q, rows(M, K, F32), wq, s, z)
 
 
 def test_offsets_past_32_bits(q):
@@ -103,6 +105,41 @@ def test_one_input_at_a_time_is_exact(q):
         R.within(y, ref, 2 * R.U * ref.abs(), f"k {m0}..")
 
 
+def test_one_input_at_a_time_few_rows(q):
+    """The same for one and two rows, where activations enter as 32-bit (bf16: 24-bit) integers
+    of their group: the largest one is exact."""
+    N, K, G = 32, 512, 64
+    for zero in (False, True):
+        wq, s, z = weights(N, K, G, zero=zero)
+        for k in list(range(0, K, 37)) + [K - 1]:
+            for dt in (F32, BF):
+                x = torch.zeros(2, K, device="cuda", dtype=dt)
+                x[0, k] = -(1.0 + torch.rand(1, device="cuda", generator=gen(k)).item())
+                x[1, K - 1 - k] = 1.9921875 if dt == BF else 2.0 - 2.0 ** -23
+                y = q.qvla_w4a16_gemv(x, wq, s, z, out_dtype=F32)
+                ref, _ = R.gemv(x, wq, s, z)
+                # scaling rounds once, the planes' sum once, the smaller planes below 2^-6 of both
+                R.within(y, ref, (2 + 2.0 ** -5) * R.U * ref.abs(), f"k {k} {dt}")
+
+
+@pytest.mark.parametrize("M", [1, 2, 3])
+@pytest.mark.parametrize("big", [30.0, 1e4, 1e8])
+def test_outliers_next_to_small_values(q, M, big):
+    """A group's largest value sets the grid of its others for one and two rows: their error is
+    counted in 2^-23 (bf16) and 2^-30 (fp32) of it."""
+    N, K, G = 64, 512, 128
+    wq, s, z = weights(N, K, G, zero=True)
+    for dt in (BF, F32):
+        x = rows(M, K, dt)
+        x[:, ::G] *= big
+        y = q.qvla_w4a16_gemv(x, wq, s, z, out_dtype=F32)
+        ref, slack = R.gemv(x, wq, s, z)
+        w = ((R.unpack(wq, False).view(N, K // G, G) - z.double()[..., None]) * s.double()[..., None]).abs().sum(2)
+        top = x.double().abs().view(M, K // G, G).amax(2)
+        grid = 2.0 ** -23 if dt == BF else 2.0 ** -30
+        R.within(y, ref, slack + grid * (top @ w.T), f"{dt}")
+
+
 def test_extreme_activations(q):
     """The largest finite fp32 values and values below bf16's normal range; an infinite or NaN
     row leaves the others alone."""
@@ -128,8 +165,11 @@ def test_rows_do_not_depend_on_the_batch(q):
     for dt in (BF, F32):
         x = rows(40, 1024, dt)
         whole = q.qvla_w4a16_gemv(x, wq, s, z, out_dtype=F32)
-        for M in (1, 8, 9, 17):
+        for M in (3, 8, 9, 17):
             assert torch.equal(q.qvla_w4a16_gemv(x[:M], wq, s, z, out_dtype=F32), whole[:M])
+        two = q.qvla_w4a16_gemv(x[:2], wq, s, z, out_dtype=F32)
+        assert torch.equal(q.qvla_w4a16_gemv(x[:1], wq, s, z, out_dtype=F32), two[:1])
+        assert torch.equal(q.qvla_w4a16_gemv(x[1:2], wq, s, z, out_dtype=F32), two[1:])
 
 
 def test_pitches_and_given_output(q):

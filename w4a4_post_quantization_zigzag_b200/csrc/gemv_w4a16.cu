@@ -5,6 +5,9 @@
 #include "qvla_common.cuh"
 #include "qvla_internal.h"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace qvla {
 namespace {
 
@@ -57,60 +60,151 @@ __global__ void __launch_bounds__(256) pack_w4g_kernel(const float* __restrict__
 }
 
 // ---------------------------------------------------------------- product
-// Bound by reading the codes once.  A warp multiplies 32 weight rows with 8 MT
-// activation rows on the warp-level tensor cores: the codes become exact bf16
-// values (u - z) in registers, x enters as bf16 (fp32 x as three bf16 parts
-// whose sum is x), every product is exact, a group's sum is fp32 and is scaled
-// once.  The order of K inside an MMA is free as long as both operands agree,
-// so a lane takes the codes as they lie in memory, eight per 32-bit word, and
-// the activations as 16-byte loads.
+// Bound by reading the codes once, so the work per code has to be small.  Two
+// kernels share the way the codes come and how work is dealt; one multiplies
+// in integers and serves one and two activation rows, the other in bf16 and
+// serves more.  (Per 32 x 256 codes the integer kernel spends about 230
+// warp instructions on the codes and 27 per row, the bf16 kernel 470 and 13.
+// 2048 -> 131072, groups of 128: one row 24.9 against 34.3 us, eight rows 42
+// against 39 us; 4096 -> 1024, eight rows: 8.5 against 4.1 us.)
 //
-// A CTA has WR x WK warps: WR bands of 32 rows, K dealt to WK warps in chunks
+// A warp multiplies bands of 32 weight rows.  A CTA has WR x WK warps: WR
+// groups that take bands in turn, K dealt to the WK warps of a group in chunks
 // of 256 (one 128-byte line of codes per row), and with few rows also to the
-// KC CTAs of a cluster; partial sums meet in shared memory (and the cluster's)
-// in a fixed order.  CTAs stay and walk over the bands, and each warp's ring
-// of code chunks (cp.async, three stages) runs on across them.
+// KC CTAs of a cluster; partial sums meet in shared memory in a fixed order.
+// Each warp feeds itself: one lane asks TMA for 32 rows x 128 bytes per chunk
+// into the warp's own ring, which runs on across bands.
 constexpr int kChunk = 256;           // K of a ring stage
-constexpr int kStages = 3;
 constexpr int kStageBytes = 32 * kChunk / 2;
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 16;
+constexpr int kStages = 3;
+constexpr int kMaxSmem = 226 * 1024;
 
 struct GemvShape {
   int WR, WK, KC;
+  int stages;            // of each warp's ring
+  int rows;              // activation rows of a pass
 };
 
-QVLA_DEVICE void cp_async16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
-               : "memory");
-}
-QVLA_DEVICE void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                     uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-QVLA_DEVICE uint32_t sub2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-// Codes j and j + 4 of a word, as bf16 values less z: 128 + u is the bf16 with
-// u in its low mantissa bits (`flip` holds 0x4300 and, for two's complement,
-// the bit that turns a code into code + 8); `zero` is 128 + z twice.
-QVLA_DEVICE void expand(uint32_t w, uint32_t flip, uint32_t zero, uint32_t (&e)[4]) {
+// What both kernels know about a warp's share of the work.
+struct Share {
+  int wk, wr, kc;        // this warp's place
+  int first, stride, per_band;     // its chunks of K
+  int band0, band_step, bands;     // its bands
+  int total;             // chunks in all
+  QVLA_DEVICE Share(const GemvArgs& a, const GemvShape& sh, int warp) {
+    wk = warp % sh.WK;
+    wr = warp / sh.WK;
+    kc = sh.KC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int chunks = (a.K + kChunk - 1) / kChunk;
+    first = kc * sh.WK + wk;
+    stride = sh.KC * sh.WK;
+    per_band = first < chunks ? (chunks - first + stride - 1) / stride : 0;
+    // bands are dealt to CTAs (clusters) one by one, a CTA's to its WR groups
+    bands = (a.N + 31) / 32;
+    const int step = gridDim.x / sh.KC;
+    band0 = blockIdx.x / sh.KC + wr * step;
+    band_step = step * sh.WR;
+    total = band0 < bands ? per_band * ((bands - band0 + band_step - 1) / band_step) : 0;
+  }
+};
+
+// A warp's ring of code chunks.
+struct Ring {
+  uint8_t* mem;
+  uint64_t* bars;
+  int stages, fetched, f_band, f_i;
+  int stage;
+  uint32_t phase;
+  bool ok;               // no wait has expired; else where one did:
+  int lost_stage;
+  uint32_t lost_phase;
+
+  // Before the previous kernel's end: barriers, and the first codes on their
+  // way to L2.
+  QVLA_DEVICE void open(uint8_t* m, uint64_t* b, int s, const Share& w, const CUtensorMap& codes, int lane) {
+    mem = m;
+    bars = b;
+    stages = s;
+    fetched = f_i = stage = 0;
+    f_band = w.band0;
+    phase = 0;
+    ok = true;
+    lost_stage = 0;
+    lost_phase = 0;
+    if (lane == 0) {
+      for (int i = 0; i < stages; ++i) mbar_init(&bars[i], 1);
+      fence_mbar_init();
+      for (int i = 0; i < stages && i < w.per_band && w.total; ++i)
+        tma_prefetch_l2_2d(&codes, (w.first + i * w.stride) * (kChunk / 2), w.band0 * 32);
+    }
+    __syncwarp();
+  }
+  QVLA_DEVICE void fetch(int to, const Share& w, const CUtensorMap& codes, int lane) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars[to], kStageBytes);
+      tma_load_2d(mem + to * kStageBytes, &codes, &bars[to], (w.first + f_i * w.stride) * (kChunk / 2),
+                  f_band * 32);
+    }
+    ++fetched;
+    if (++f_i == w.per_band) {
+      f_i = 0;
+      f_band += w.band_step;
+    }
+  }
+  QVLA_DEVICE void fill(const Share& w, const CUtensorMap& codes, int lane) {
+    for (int s = 0; s < stages - 1; ++s)
+      if (fetched < w.total) fetch(s, w, codes, lane);
+  }
+  // Waits for the next chunk and asks for the one that takes the place of the
+  // last (every lane has read that when all have come here).
+  QVLA_DEVICE void next(const Share& w, const CUtensorMap& codes, int lane, unsigned int* err) {
+    if (ok) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[stage], phase, err));
+      if (!ok) {
+        lost_stage = stage;
+        lost_phase = phase;
+      }
+    }
+    if (ok && fetched < w.total) fetch(stage == 0 ? stages - 1 : stage - 1, w, codes, lane);
+  }
+  QVLA_DEVICE void done() {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  // After an expired wait: one more limit for the copies in flight to land.
+  QVLA_DEVICE void close(int lane, unsigned int* err) {
+    if (!ok && lane == 0)
+      for (int s = 0; s < stages; ++s) mbar_wait(&bars[s], lost_phase ^ (s < lost_stage), err);
+  }
+};
+
+// The MMA's row g is row rho(g) of eight: with TMA's 128-byte swizzle, lanes
+// that read 4, 8 or 16 bytes of 8, 4 or 2 rows at once then meet no bank twice.
+QVLA_DEVICE int rho_of(int g) { return (g & 1) << 2 | (g & 2) | (g >> 2 & 1); }
+
+// Words of eight codes of rows rho + 8 r in segment `seg` of a stage: kWords
+// words per lane quad member t.
+template <int kSeg, int kWords>
+QVLA_DEVICE void load_codes(uint32_t stage, int seg, int rho, int t, uint32_t (&w)[4][kWords]) {
+  const int byte = seg * (kSeg / 2) + t * 4 * kWords;
+  const uint32_t at = stage + rho * 128 + ((byte >> 4) ^ rho) * 16 + (byte & 15);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) e[j] = sub2((w >> (4 * j) & 0x000f000fu) ^ flip, zero);
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t from = at + r * 1024;
+    if constexpr (kWords == 4) {
+      const uint4 v = lds128(from);
+      w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+    } else if constexpr (kWords == 2) {
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[r][0]), "=r"(w[r][1]) : "r"(from) : "memory");
+    } else {
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[r][0]) : "r"(from) : "memory");
+    }
+  }
 }
-// The bf16 values below two fp32 values (cut, not rounded: no value overflows)
-// side by side, and what they leave.
-QVLA_DEVICE uint32_t take2(float& lo, float& hi) {
-  const uint32_t a = __float_as_uint(lo) & 0xffff0000u, b = __float_as_uint(hi) & 0xffff0000u;
-  lo -= __uint_as_float(a);
-  hi -= __uint_as_float(b);
-  return a >> 16 | b;
-}
+
 QVLA_DEVICE float scale_at(const GemvArgs& a, int64_t i) {
   return a.sdt == QVLA_DTYPE_F32 ? static_cast<const float*>(a.scale)[i]
                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(a.scale)[i]);
@@ -120,19 +214,13 @@ QVLA_DEVICE float scale_at(const GemvArgs& a, int64_t i) {
 template <int NG>
 struct RowGroups {
   float s[NG];
-  uint32_t z[NG];        // 128 + z as two bf16
+  float z[NG];
 };
 
-template <int NG>
+template <int NG, bool ZERO>
 QVLA_DEVICE void load_groups(const GemvArgs& a, int n, int c, RowGroups<NG>& r) {
   const int groups = a.K / a.group;
   const int64_t at = static_cast<int64_t>(n) * groups + c * NG;
-#pragma unroll
-  for (int j = 0; j < NG; ++j) {
-    r.s[j] = 0.f;
-    r.z[j] = a.zero ? 0x43004300u : 0x43084308u;
-  }
-  if (n >= a.N) return;
   if (groups % NG == 0) {
     // every row's chunk is whole and starts at a multiple of its size
     if (a.sdt == QVLA_DTYPE_F32) {
@@ -168,20 +256,19 @@ QVLA_DEVICE void load_groups(const GemvArgs& a, int n, int c, RowGroups<NG>& r) 
         r.s[0] = __bfloat162float(*p);
       }
     }
-    if (a.zero) {
+    if constexpr (ZERO) {
       const uint8_t* p = a.zero + at;
-      uint64_t w;
+      uint32_t w[2] = {0u, 0u};
       if constexpr (NG == 8)
-        w = *reinterpret_cast<const uint64_t*>(p);
+        *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
       else if constexpr (NG == 4)
-        w = *reinterpret_cast<const uint32_t*>(p);
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
       else if constexpr (NG == 2)
-        w = *reinterpret_cast<const uint16_t*>(p);
+        w[0] = *reinterpret_cast<const uint16_t*>(p);
       else
-        w = *p;
+        w[0] = *p;
 #pragma unroll
-      for (int j = 0; j < NG; ++j)
-        r.z[j] = 0x43004300u + (static_cast<uint32_t>(w >> (8 * j)) & 15u) * 0x10001u;
+      for (int j = 0; j < NG; ++j) r.z[j] = static_cast<float>(w[j >> 2] >> (8 * (j & 3)) & 15u);
     }
     return;
   }
@@ -189,8 +276,424 @@ QVLA_DEVICE void load_groups(const GemvArgs& a, int n, int c, RowGroups<NG>& r) 
   for (int j = 0; j < NG; ++j)
     if (c * NG + j < groups) {
       r.s[j] = scale_at(a, at + j);
-      if (a.zero) r.z[j] = 0x43004300u + (a.zero[at + j] & 15u) * 0x10001u;
+      if constexpr (ZERO) r.z[j] = static_cast<float>(a.zero[at + j] & 15u);
     }
+}
+
+QVLA_DEVICE void store_y(const GemvArgs& a, int m, int n, float v) {
+  if (a.bias) v += a.bias[n];
+  const int64_t o = static_cast<int64_t>(m) * a.ldy + n;
+  if (a.ydt == QVLA_DTYPE_F32)
+    static_cast<float*>(a.y)[o] = v;
+  else
+    static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
+}
+
+// ---- the end of a band: y[m] of weight row `lane`, for each of the pass's
+// rows, summed over the WK warps, then over the cluster, and stored.
+// red [W][rows][32], far [KC][rows][32].
+template <int kRows>
+QVLA_DEVICE void finish_band(const GemvArgs& a, const GemvShape& sh, const Share& w, int band, int warp, int lane,
+                             int m0, int rows, const float (&y)[kRows], float* red, float* far) {
+  const int row = band * 32 + lane;
+  if (sh.WK == 1 && sh.KC == 1) {
+#pragma unroll
+    for (int m = 0; m < kRows; ++m)
+      if (m < rows && row < a.N) store_y(a, m0 + m, row, y[m]);
+    return;
+  }
+  if (sh.WK > 1) {
+#pragma unroll
+    for (int m = 0; m < kRows; ++m)
+      if (m < rows) red[(warp * sh.rows + m) * 32 + lane] = y[m];
+    named_barrier(1 + w.wr, 32 * sh.WK);
+  }
+  uint32_t to = 0;
+  if (sh.KC > 1) {
+    // one band per cluster (WR = 1): each CTA's sums go to the first one
+    to = map_shared_rank(smem_u32(far + w.kc * sh.rows * 32), 0);
+    cluster_wait();
+  }
+  if (sh.WK > 1) {
+    for (int m = w.wk; m < rows; m += sh.WK) {
+      float v = 0.f;
+      for (int k = 0; k < sh.WK; ++k) v += red[((w.wr * sh.WK + k) * sh.rows + m) * 32 + lane];
+      if (sh.KC > 1)
+        st_shared_cluster_f32(to + (m * 32 + lane) * 4, v);
+      else if (row < a.N)
+        store_y(a, m0 + m, row, v);
+    }
+  } else {
+#pragma unroll
+    for (int m = 0; m < kRows; ++m)
+      if (m < rows) st_shared_cluster_f32(to + (m * 32 + lane) * 4, y[m]);
+  }
+  if (sh.KC > 1) {
+    cluster_sync();
+    if (w.kc == 0)
+      for (int m = w.wk; m < rows; m += sh.WK) {
+        float v = 0.f;
+        for (int r = 0; r < sh.KC; ++r) v += far[(r * sh.rows + m) * 32 + lane];
+        if (row < a.N) store_y(a, m0 + m, row, v);
+      }
+  } else if (band + w.band_step < w.bands) {
+    named_barrier(1 + w.wr, 32 * sh.WK);       // the sums may be overwritten after this
+  }
+}
+
+// A warp's tile [8][32] of sums (columns x weight rows), transposed from the
+// MMA's lanes: the lane's own weight row of each column.
+QVLA_DEVICE void turn_tile(float* tile, const float (&lo)[4], const float (&hi)[4], int rho, int t, int lane,
+                           float (&v)[8]) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    tile[(2 * t + (j & 1)) * 32 + ((rho + (j >> 1) * 8) ^ 8 * t)] = lo[j];
+    tile[(2 * t + (j & 1)) * 32 + ((16 + rho + (j >> 1) * 8) ^ 8 * t)] = hi[j];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = tile[q * 32 + (lane ^ 8 * (q / 2))];
+}
+
+// ============================================================ one or two rows
+// Within a group, an activation row is a row of integers X = rint(x 2^e), e set
+// by the group's largest |x|: 24 bits for bf16 x, 32 for fp32 x, split into
+// ND = 3 or 4 signed bytes, X = sum_j 2^(8j) d_j.  Each byte plane is a column
+// of the right operand (six or eight of the MMA's eight for two rows).  The
+// codes become bytes by a mask and a shift, eight codes in three instructions;
+// sum u d is exact in 32 bits; once per group it is scaled by s 2^(8j - e) and
+// added in fp32, and at the end a row's planes are added, the smallest first.
+//
+// What rounding x to its group's grid costs: at most 2^-23 (bf16) or 2^-30
+// (fp32) of the group's largest |x| per element, what an fp32 sum that holds
+// that element may lose with every addition.  bf16 values within 2^14 of the
+// largest, and fp32 values within 2^6, are not rounded at all.
+//
+// The planes are laid out in shared memory once per CTA, while the first codes
+// come.
+
+// D = A B + C, 16 x 8 x 32, signed bytes, 32-bit sums.
+QVLA_DEVICE void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with every sum starting at c0.
+QVLA_DEVICE void mma_s8_from(int (&c)[4], int c0, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0));
+}
+
+QVLA_DEVICE float pow2(int e) {                // 2^e for e in [-149, 127]
+  return e >= -126 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23)
+                   : __uint_as_float(1u << (e + 149));
+}
+
+// One lane's eight activations (chunk octet `lane`) as byte planes.  `mag` is
+// the largest |x| of the group (bits); returns e, the group's exponent.
+// planes[j] = {bytes of x 0, 2, 4, 6, bytes of x 1, 3, 5, 7}: the order in
+// which a code word's masks give the codes.
+template <int ND>
+QVLA_DEVICE int byte_planes(const float (&x)[8], uint32_t mag, uint2 (&planes)[ND]) {
+  // ND = 3: the top byte holds 127 2^16 + ...: the last 1/128 below a power of
+  // two takes the next exponent
+  const int p = static_cast<int>((mag + (ND == 3 ? 0x10000u : 0u)) >> 23) - 127;
+  const int e = min((ND == 3 ? 22 : 29) - p, 145);
+  const float f0 = pow2(e >> 1), f1 = pow2(e - (e >> 1));
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    constexpr uint32_t bias = ND == 3 ? 0x00808080u : 0x80808080u;
+    const int X = mag < 0x7f800000u ? __float2int_rn(x[i] * f0 * f1) : 0;
+    b[i] = (static_cast<uint32_t>(X) + bias) ^ bias;       // two's complement bytes with carries
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo01 = __byte_perm(b[h], b[h + 2], 0x5140);       // bytes 0, 0, 1, 1
+    const uint32_t lo23 = __byte_perm(b[h + 4], b[h + 6], 0x5140);
+    const uint32_t hi01 = __byte_perm(b[h], b[h + 2], 0x7362);       // bytes 2, 2, 3, 3
+    const uint32_t hi23 = __byte_perm(b[h + 4], b[h + 6], 0x7362);
+    uint32_t w[4] = {__byte_perm(lo01, lo23, 0x5410), __byte_perm(lo01, lo23, 0x7632),
+                     __byte_perm(hi01, hi23, 0x5410), __byte_perm(hi01, hi23, 0x7632)};
+#pragma unroll
+    for (int j = 0; j < ND; ++j) (h ? planes[j].y : planes[j].x) = w[j];
+  }
+  return e;
+}
+
+// Shared memory: rings, byte planes, their factors (and sums, with zero
+// points), a transposing tile per warp, sums of the WK warps and of the cluster.
+struct PlaneLayout {
+  int slots, cols, pairs;
+  uint32_t planes, factors, tile, red, far, bytes;
+};
+
+__host__ __device__ inline PlaneLayout plane_layout(const GemvShape& sh, int K, int G, int ND, bool zero) {
+  PlaneLayout l;
+  const int W = sh.WR * sh.WK, chunks = (K + kChunk - 1) / kChunk;
+  l.slots = (chunks + sh.KC * sh.WK - 1) / (sh.KC * sh.WK) * sh.WK;
+  l.cols = sh.rows * ND;
+  l.pairs = (l.cols + 1) / 2;
+  l.planes = W * sh.stages * kStageBytes;
+  l.factors = l.planes + l.slots * kChunk * l.cols;
+  l.tile = l.factors + l.slots * (kChunk / G) * l.pairs * (zero ? 16 : 8);
+  l.tile = (l.tile + 15) & ~15u;
+  l.red = l.tile + W * 1024;
+  l.far = l.red + (sh.WK > 1 ? W * sh.rows * 128 : 0);
+  l.bytes = l.far + (sh.KC > 1 ? sh.KC * sh.rows * 128 : 0) + 1024;   // + alignment of the rings
+  return l;
+}
+
+// Rows past N are computed from the zeros that TMA fills in, columns past the
+// last plane repeat it; neither is stored, and rows and columns of the product
+// do not mix.  K ends with a group, so the last chunk's loop just ends early.
+template <int G, int ND, bool ZERO>
+__global__ void __launch_bounds__(32 * kMaxWarps, 1)
+    gemv_planes_kernel(const __grid_constant__ GemvArgs a, const __grid_constant__ GemvShape sh,
+                       const __grid_constant__ CUtensorMap codes, unsigned int* err) {
+  constexpr int kSeg = G < 128 ? G : 128;      // K of one lane quad's load
+  constexpr int kSegs = kChunk / kSeg;
+  constexpr int kWords = kSeg / 32;            // words of eight codes per lane and load
+  constexpr int NG = kChunk / G;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kMaxWarps][kStages];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, rho = rho_of(g);
+  const Share w(a, sh, warp);
+  const int m0 = blockIdx.y * sh.rows, rows = min(sh.rows, a.M - m0), cols = rows * ND;
+  const PlaneLayout at = plane_layout(sh, a.K, G, ND, ZERO);
+  uint8_t* planes = smem + at.planes;
+  // [slot][NG][pair of columns]: their factors and, with zero points, sums
+  float* factors = reinterpret_cast<float*>(smem + at.factors);
+  constexpr int kPair = ZERO ? 4 : 2;
+  float* tile = reinterpret_cast<float*>(smem + at.tile) + warp * 256;
+  Ring ring;
+  ring.open(smem + warp * sh.stages * kStageBytes, bars[warp], sh.stages, w, codes, lane);
+  if (sh.KC > 1) cluster_arrive_relaxed();     // every CTA of the cluster runs before any writes to another
+  pdl_launch_dependents();
+  pdl_wait();
+  ring.fill(w, codes, lane);
+  RowGroups<NG> next = {};
+  if (w.total) load_groups<NG, ZERO>(a, min(w.band0 * 32 + lane, a.N - 1), w.first, next);
+
+  // ---- the byte planes of x: the chunks of this warp's share of K, dealt to
+  // the WR warps that use them; slot i WK + wk is chunk first + i stride
+  using X = std::conditional_t<ND == 3, uint4, float4>;
+  constexpr int kVecs = ND == 3 ? 1 : 2, kBatch = ND == 3 ? 4 : 2;
+  const int units = w.per_band * rows;
+  for (int u0 = w.wr; u0 < units; u0 += sh.WR * kBatch) {
+    X raw[kBatch][kVecs];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int u = u0 + q * sh.WR, i = u / rows, k = (w.first + i * w.stride) * kChunk + lane * 8;
+      const int64_t src = static_cast<int64_t>(m0 + u - i * rows) * a.ldx + k;
+#pragma unroll
+      for (int h = 0; h < kVecs; ++h) {
+        raw[q][h] = X{};
+        if (u < units && k < a.K)
+          raw[q][h] = ND == 3 ? *reinterpret_cast<const X*>(static_cast<const __nv_bfloat16*>(a.x) + src)
+                              : reinterpret_cast<const X*>(static_cast<const float*>(a.x) + src)[h];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int u = u0 + q * sh.WR;
+      if (u >= units) break;
+      const int i = u / rows, m = u - i * rows;
+      float x[8];
+      if constexpr (ND == 3) {
+        const uint32_t h[4] = {raw[q][0].x, raw[q][0].y, raw[q][0].z, raw[q][0].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[2 * j] = __uint_as_float(h[j] << 16);
+          x[2 * j + 1] = __uint_as_float(h[j] & 0xffff0000u);
+        }
+      } else {
+        const X v = raw[q][0], w = raw[q][kVecs - 1];
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+      }
+      uint32_t mag = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mag = max(mag, __float_as_uint(x[j]) & 0x7fffffffu);
+#pragma unroll
+      for (int d = 1; d < G / 8; d <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
+      uint2 pl[ND];
+      const int e = byte_planes<ND>(x, mag, pl);
+      // this lane's octet is word j of quad lane y in segment seg
+      const int seg = lane / (kSeg / 8), y = lane % (kSeg / 8) / kWords, j = lane % kWords;
+      const int slot = i * sh.WK + w.wk, grp = lane / (G / 8);
+      uint8_t* chunk = planes + static_cast<size_t>(slot) * kChunk * at.cols;
+      const bool bad = mag >= 0x7f800000u;
+#pragma unroll
+      for (int p = 0; p < ND; ++p) {
+        const int col = m * ND + p;
+        if constexpr (kWords == 1)
+          *reinterpret_cast<uint2*>(chunk + (seg * at.cols + col) * 32 + y * 8) = pl[p];
+        else
+          *reinterpret_cast<uint2*>(chunk + ((seg * (kWords / 2) + j / 2) * at.cols + col) * 64 + y * 16 +
+                                    j % 2 * 8) = pl[p];
+        int sum = 0;
+        if constexpr (ZERO) {
+          sum = __dp4a(static_cast<int>(pl[p].x), 0x01010101, __dp4a(static_cast<int>(pl[p].y), 0x01010101, 0));
+#pragma unroll
+          for (int d = 1; d < G / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        }
+        if (lane % (G / 8) == 0) {
+          // two's complement codes enter as 16 times their value
+          float* to = factors + ((slot * NG + grp) * at.pairs + col / 2) * kPair + col % 2;
+          to[0] = bad ? __uint_as_float(0x7fc00000u) : pow2(8 * p - e - (ZERO ? 0 : 4));
+          if constexpr (ZERO) to[2] = static_cast<float>(sum);
+        }
+      }
+    }
+  }
+  if (sh.WR > 1)
+    __syncthreads();
+  else
+    __syncwarp();
+
+  // this lane's column as operand, its pair of columns as result
+  const int col_b = min(g, cols - 1) * (kWords == 1 ? 32 : 64) + t * (kWords == 1 ? 8 : 16);
+  const int pair_c = min(t, at.pairs - 1) * kPair;
+  constexpr uint32_t mask = ZERO ? 0x0f0f0f0fu : 0xf0f0f0f0u;
+  for (int band = w.band0; band < w.bands; band += w.band_step) {
+    float acc[2][4] = {};
+#pragma unroll 1
+    for (int i = 0; i < w.per_band; ++i) {
+      const int c = w.first + i * w.stride, slot = i * sh.WK + w.wk;
+      ring.next(w, codes, lane, err);
+      const RowGroups<NG> rg = next;
+      if (i + 1 < w.per_band)
+        load_groups<NG, ZERO>(a, min(band * 32 + lane, a.N - 1), c + w.stride, next);
+      else if (band + w.band_step < w.bands)
+        load_groups<NG, ZERO>(a, min((band + w.band_step) * 32 + lane, a.N - 1), w.first, next);
+      const uint32_t stage = smem_u32(ring.mem) + ring.stage * kStageBytes;
+      const uint8_t* chunk = planes + static_cast<size_t>(slot) * kChunk * at.cols;
+      int part[2][4];
+#pragma unroll
+      for (int seg = 0; seg < kSegs; ++seg) {
+        if (c * kChunk + seg * kSeg >= a.K) break;
+        const int grp = seg * kSeg / G;
+        uint32_t u[4][kWords];
+        load_codes<kSeg, kWords>(stage, seg, rho, t, u);
+#pragma unroll
+        for (int j2 = 0; j2 < (kWords + 1) / 2; ++j2) {
+          uint32_t b[2][2];
+          if constexpr (kWords == 1) {
+            const uint2 v = *reinterpret_cast<const uint2*>(chunk + seg * at.cols * 32 + col_b);
+            b[0][0] = v.x, b[0][1] = v.y;
+          } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                chunk + (seg * (kWords / 2) + j2) * at.cols * 64 + col_b);
+            b[0][0] = v.x, b[0][1] = v.y, b[1][0] = v.z, b[1][1] = v.w;
+          }
+#pragma unroll
+          for (int jj = 0; jj < (kWords == 1 ? 1 : 2); ++jj) {
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t v = u[r][2 * j2 + jj];
+              lo[r] = (ZERO ? v : v << 4) & mask;
+              hi[r] = (ZERO ? v >> 4 : v) & mask;
+            }
+            // a sum that starts at the bits of 1.5 2^23 ends as the bits of
+            // 1.5 2^23 + itself (|sum| <= 256 * 128 * 128)
+            const bool opens = seg * kSeg % G == 0 && j2 == 0 && jj == 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (opens)
+                mma_s8_from(part[h], 0x4b400000, lo[2 * h], lo[2 * h + 1], hi[2 * h], hi[2 * h + 1], b[jj][0],
+                            b[jj][1]);
+              else
+                mma_s8(part[h], lo[2 * h], lo[2 * h + 1], hi[2 * h], hi[2 * h + 1], b[jj][0], b[jj][1]);
+            }
+          }
+        }
+        if ((seg + 1) * kSeg % G == 0) {
+          const float* fp = factors + (slot * NG + grp) * at.pairs * kPair + pair_c;
+          const float2 f = *reinterpret_cast<const float2*>(fp);
+          float2 sum = {};
+          if constexpr (ZERO) sum = *reinterpret_cast<const float2*>(fp + 2);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float s = __shfl_sync(0xffffffffu, rg.s[grp], rho + 16 * h + 8 * r);
+              float v0 = __int_as_float(part[h][2 * r]) - 12582912.f;
+              float v1 = __int_as_float(part[h][2 * r + 1]) - 12582912.f;
+              if constexpr (ZERO) {                      // exact: below 2^22
+                const float z = __shfl_sync(0xffffffffu, rg.z[grp], rho + 16 * h + 8 * r);
+                v0 = fmaf(-z, sum.x, v0);
+                v1 = fmaf(-z, sum.y, v1);
+              }
+              acc[h][2 * r] = fmaf(v0 * s, f.x, acc[h][2 * r]);
+              acc[h][2 * r + 1] = fmaf(v1 * s, f.y, acc[h][2 * r + 1]);
+            }
+        }
+      }
+      ring.done();
+    }
+    float v[8], y[2] = {};
+    turn_tile(tile, acc[0], acc[1], rho, t, lane, v);
+#pragma unroll
+    for (int q = 0; q < 2 * ND; ++q) y[q / ND] += v[q];
+    finish_band(a, sh, w, band, warp, lane, m0, rows, y, reinterpret_cast<float*>(smem + at.red),
+                reinterpret_cast<float*>(smem + at.far));
+  }
+  ring.close(lane, err);
+}
+
+// ============================================================== three and more
+// The codes become exact bf16 values (u - z) in registers, x enters as bf16
+// (fp32 x as three bf16 parts whose sum is x), every product is exact, a
+// group's sum is fp32 and is scaled once.  The order of K inside an MMA is free
+// as long as both operands agree, so a lane takes the codes as they lie in
+// memory, eight per 32-bit word, and meets them with activations in that order.
+
+QVLA_DEVICE void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from a zero sum.
+QVLA_DEVICE void mma_bf16_from0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+QVLA_DEVICE uint32_t sub2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Codes j and j + 4 of a word, as bf16 values less z: 128 + u is the bf16 with
+// u in its low mantissa bits (`flip` holds 0x4300 and, for two's complement,
+// the bit that turns a code into code + 8); `zero` is 128 + z twice.
+QVLA_DEVICE void expand(uint32_t w, uint32_t flip, uint32_t zero, uint32_t (&e)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) e[j] = sub2((w >> (4 * j) & 0x000f000fu) ^ flip, zero);
+}
+// The bf16 values below two fp32 values (cut, not rounded: no value overflows)
+// side by side, and what they leave.
+QVLA_DEVICE uint32_t take2(float& lo, float& hi) {
+  const uint32_t a = __float_as_uint(lo) & 0xffff0000u, b = __float_as_uint(hi) & 0xffff0000u;
+  lo -= __uint_as_float(a);
+  hi -= __uint_as_float(b);
+  return a >> 16 | b;
 }
 
 // Eight activations of a row in the order of expand(): XP parts of the pairs
@@ -199,261 +702,217 @@ template <int XP>
 struct Acts {
   uint32_t p[XP][4];
 };
-template <int XP>
-QVLA_DEVICE Acts<XP> load_acts(const void* x, int64_t at, bool in) {
-  Acts<XP> r = {};
-  if (!in) return r;
+template <int XP, typename X>
+QVLA_DEVICE Acts<XP> load_acts(const X* x) {
+  Acts<XP> r;
+  const uint4 v = reinterpret_cast<const uint4*>(x)[0];
   if constexpr (XP == 1) {
-    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at);
     r.p[0][0] = __byte_perm(v.x, v.z, 0x5410);
     r.p[0][1] = __byte_perm(v.x, v.z, 0x7632);
     r.p[0][2] = __byte_perm(v.y, v.w, 0x5410);
     r.p[0][3] = __byte_perm(v.y, v.w, 0x7632);
   } else {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    float4 lo = q[0], hi = q[1];
+    const uint4 u = reinterpret_cast<const uint4*>(x)[1];
+    float lo[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+    float hi[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
 #pragma unroll
-    for (int p = 0; p < XP; ++p) {
-      r.p[p][0] = take2(lo.x, hi.x);
-      r.p[p][1] = take2(lo.y, hi.y);
-      r.p[p][2] = take2(lo.z, hi.z);
-      r.p[p][3] = take2(lo.w, hi.w);
-    }
+    for (int p = 0; p < XP; ++p)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.p[p][j] = take2(lo[j], hi[j]);
   }
   return r;
 }
 
-// 16-byte unit of a row in its 128-byte line of a stage: lanes that read 4, 8
-// or 16 bytes of 8, 4 or 2 rows at once meet no bank twice (the row's three
-// low bits, reversed).
-QVLA_DEVICE int unit_at(int row, int unit) {
-  return unit ^ ((row & 1) << 2 | (row & 2) | (row >> 2 & 1));
+// Shared memory: rings, a transposing tile per warp, sums of the WK warps and
+// of the cluster, the activations in operand order if they are staged.
+struct PartLayout {
+  uint32_t tile, red, far, acts, bytes;
+};
+
+__host__ __device__ inline PartLayout part_layout(const GemvShape& sh, int K, int XP, bool staged) {
+  PartLayout l;
+  const int W = sh.WR * sh.WK;
+  l.tile = W * sh.stages * kStageBytes;
+  l.red = l.tile + W * 1024;
+  l.far = l.red + (sh.WK > 1 ? W * sh.rows * 128 : 0);
+  l.acts = l.far + (sh.KC > 1 ? sh.KC * sh.rows * 128 : 0);
+  l.bytes = l.acts + (staged ? K * sh.rows * 2 * XP : 0) + 1024;
+  return l;
 }
 
-template <int G, int MT, int XP>
-__global__ void __launch_bounds__(32 * kMaxWarps, MT <= 2 ? 2 : 1)
-    gemv_kernel(const __grid_constant__ GemvArgs a, const __grid_constant__ GemvShape sh) {
-  constexpr int kSeg = G < 128 ? G : 128;      // K of one lane quad's load
-  constexpr int kWords = kSeg / 32;            // words of eight codes per lane and load
+// As above; columns past the last activation row repeat it and are not stored.
+template <int G, int MT, int XP, bool STAGED>
+__global__ void __launch_bounds__(32 * kMaxWarps, 1)
+    gemv_parts_kernel(const __grid_constant__ GemvArgs a, const __grid_constant__ GemvShape sh,
+                      const __grid_constant__ CUtensorMap codes, unsigned int* err) {
+  using X = std::conditional_t<XP == 1, __nv_bfloat16, float>;
+  constexpr int kSeg = G < 128 ? G : 128;
+  constexpr int kSegs = kChunk / kSeg;
+  constexpr int kWords = kSeg / 32;
   constexpr int NG = kChunk / G;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int wk = warp % sh.WK, wr = warp / sh.WK, W = sh.WK * sh.WR;
-  const int kc = sh.KC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
-  float* red = reinterpret_cast<float*>(smem + W * kStages * kStageBytes);   // [W][8 MT][33]
-  constexpr int kRed = 8 * MT * 33;
-  const int chunks = (a.K + kChunk - 1) / kChunk;
-  const int first = kc * sh.WK + wk, stride = sh.KC * sh.WK;
-  const int per_tile = first < chunks ? (chunks - first + stride - 1) / stride : 0;
-  const int tiles = (a.N + 32 * sh.WR - 1) / (32 * sh.WR);
-  const int tile0 = blockIdx.x / sh.KC, tile_step = gridDim.x / sh.KC;
-  const int my_tiles = tile0 < tiles ? (tiles - tile0 + tile_step - 1) / tile_step : 0;
-  const int total = per_tile * my_tiles;
-  const int m0 = blockIdx.y * 8 * MT;
-  const int64_t pitch = a.K / 2;
-
-  // the first lines of codes start for L2 before the previous kernel's end
-  for (int i = 0; i < kStages - 1 && i < per_tile; ++i) {
-    const int64_t n = (static_cast<int64_t>(tile0) * sh.WR + wr) * 32 + lane;
-    if (total && n < a.N)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.wq + n * pitch + (first + i * stride) * 128));
-  }
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kMaxWarps][kStages];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, rho = rho_of(g);
+  const Share w(a, sh, warp);
+  const int m0 = blockIdx.y * sh.rows, cols = min(sh.rows, a.M - m0);
+  const PartLayout at = part_layout(sh, a.K, XP, STAGED);
+  float* tile = reinterpret_cast<float*>(smem + at.tile) + warp * 256;
+  uint4* xs = reinterpret_cast<uint4*>(smem + at.acts);
+  Ring ring;
+  ring.open(smem + warp * sh.stages * kStageBytes, bars[warp], sh.stages, w, codes, lane);
+  if (sh.KC > 1) cluster_arrive_relaxed();
   pdl_launch_dependents();
   pdl_wait();
-
-  int f_tile = tile0, f_i = 0;                 // next chunk to fetch
-  auto fetch = [&](int stage) {
-    const int c = first + f_i * stride;
-    const int unit = lane & 7, r0 = lane >> 3;
-    const int64_t n0 = (static_cast<int64_t>(f_tile) * sh.WR + wr) * 32 + r0;
-    const bool col = c * 128 + unit * 16 < pitch;
-    const uint8_t* src = a.wq + n0 * pitch + c * 128 + unit * 16;
-    const uint32_t dst = ring + stage * kStageBytes;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = r0 + 4 * i;
-      const bool in = col && n0 + 4 * i < a.N;
-      cp_async16(dst + row * 128 + unit_at(row, unit) * 16, in ? src + 4 * i * pitch : a.wq, in);
-    }
-    if (++f_i == per_tile) {
-      f_i = 0;
-      f_tile += tile_step;
-    }
+  ring.fill(w, codes, lane);
+  const bool zero = a.zero != nullptr;
+  const uint32_t flip = zero ? 0x43004300u : 0x43084308u;
+  RowGroups<NG> next = {};
+  auto load_next = [&](int n, int c) {
+    if (zero)
+      load_groups<NG, true>(a, min(n, a.N - 1), c, next);
+    else
+      load_groups<NG, false>(a, min(n, a.N - 1), c, next);
   };
-  int fetched = 0;
-  for (int s = 0; s < kStages - 1; ++s) {
-    if (fetched < total) {
-      fetch(s);
-      ++fetched;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+  if (w.total) load_next(w.band0 * 32 + lane, w.first);
+  const X* xrow[MT];                           // direct: this lane's place in its activation rows
+  int xcol[MT];                                // staged: its columns
+#pragma unroll
+  for (int n = 0; n < MT; ++n) {
+    xcol[n] = min(n * 8 + g, cols - 1);
+    xrow[n] = static_cast<const X*>(a.x) + static_cast<int64_t>(m0 + xcol[n]) * a.ldx + t * 8 * kWords;
   }
-  const uint32_t flip = a.zero ? 0x43004300u : 0x43084308u;
-  RowGroups<NG> next;
-  if (total) load_groups<NG>(a, (tile0 * sh.WR + wr) * 32 + lane, first, next);
-
-  int stage = 0;
-  for (int tile = tile0; tile < tiles; tile += tile_step) {
+  if constexpr (STAGED) {
+    // 16-byte pieces in the order the lanes read them: [segment, word, part][t]
+    // [column]
+    const int pieces = a.K / 8;
+    for (int i = threadIdx.x; i < pieces * cols; i += blockDim.x) {
+      const int k8 = i % pieces, col = i / pieces;
+      const int seg = k8 / (kSeg / 8), q = k8 % (kSeg / 8);
+      const Acts<XP> v =
+          load_acts<XP>(static_cast<const X*>(a.x) + static_cast<int64_t>(m0 + col) * a.ldx + k8 * 8);
+#pragma unroll
+      for (int p = 0; p < XP; ++p)
+        xs[((((seg * kWords + q % kWords) * XP + p) * 4 + q / kWords)) * cols + col] =
+            make_uint4(v.p[p][0], v.p[p][1], v.p[p][2], v.p[p][3]);
+    }
+    __syncthreads();
+  }
+  for (int band = w.band0; band < w.bands; band += w.band_step) {
     float acc[2][MT][4] = {};
-    const int n_band = (tile * sh.WR + wr) * 32;
 #pragma unroll 1
-    for (int i = 0; i < per_tile; ++i) {
-      const int c = first + i * stride;
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncwarp();
-      if (fetched < total) {
-        fetch(stage == 0 ? kStages - 1 : stage - 1);
-        ++fetched;
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+    for (int i = 0; i < w.per_band; ++i) {
+      const int c = w.first + i * w.stride;
+      ring.next(w, codes, lane, err);
       const RowGroups<NG> rg = next;
-      if (i + 1 < per_tile)
-        load_groups<NG>(a, n_band + lane, c + stride, next);
-      else if (tile + tile_step < tiles)
-        load_groups<NG>(a, ((tile + tile_step) * sh.WR + wr) * 32 + lane, first, next);
-      const uint32_t base = ring + stage * kStageBytes;
-      // fp32 x: the products of its first part apart from those of the rest
-      float part[XP > 1 ? 2 : 1][2][MT][4] = {};
+      if (i + 1 < w.per_band)
+        load_next(band * 32 + lane, c + w.stride);
+      else if (band + w.band_step < w.bands)
+        load_next((band + w.band_step) * 32 + lane, w.first);
+      const uint32_t stage = smem_u32(ring.mem) + ring.stage * kStageBytes;
+      // two chains of sums; fp32 x: its first part apart from the rest
+      float part[2][2][MT][4];
 #pragma unroll
-      for (int seg = 0; seg < kChunk / kSeg; ++seg) {
+      for (int seg = 0; seg < kSegs; ++seg) {
+        if (c * kChunk + seg * kSeg >= a.K) break;
         const int grp = seg * kSeg / G;
-        // codes of rows g, g + 8 of both halves of the band
-        uint32_t w[4][kWords];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = g + 8 * r;
-          const int byte = seg * (kSeg / 2) + t * 4 * kWords;
-          const uint32_t at = base + row * 128 + unit_at(row, byte >> 4) * 16 + (byte & 15);
-          if constexpr (kWords == 4) {
-            const uint4 v = lds128(at);
-            w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
-          } else if constexpr (kWords == 2) {
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[r][0]), "=r"(w[r][1]) : "r"(at) : "memory");
-          } else {
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[r][0]) : "r"(at) : "memory");
-          }
-        }
+        uint32_t u[4][kWords];
+        load_codes<kSeg, kWords>(stage, seg, rho, t, u);
         uint32_t z[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          z[r] = a.zero ? __shfl_sync(0xffffffffu, rg.z[grp], g + 8 * r) : 0x43084308u;
-        const int k0 = c * kChunk + seg * kSeg + t * 8 * kWords;
+        for (int r = 0; r < 4; ++r) z[r] = 0x43084308u;
+        if (zero) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            z[r] = 0x43004300u +
+                   static_cast<uint32_t>(__shfl_sync(0xffffffffu, rg.z[grp], rho + 8 * r)) * 0x10001u;
+        }
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
           uint32_t e[4][4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) expand(w[r][j], flip, z[r], e[r]);
+          for (int r = 0; r < 4; ++r) expand(u[r][j], flip, z[r], e[r]);
 #pragma unroll
           for (int n = 0; n < MT; ++n) {
-            const int m = m0 + n * 8 + g;
-            const Acts<XP> b = load_acts<XP>(a.x, static_cast<int64_t>(m) * a.ldx + k0 + 8 * j,
-                                             m < a.M && k0 + 8 * j < a.K);
+            Acts<XP> b;
+            if constexpr (STAGED) {
+              const int piece = ((c * kSegs + seg) * kWords + j) * XP * 4 + t;
+#pragma unroll
+              for (int p = 0; p < XP; ++p) {
+                const uint4 v = xs[(piece + p * 4) * cols + xcol[n]];
+                b.p[p][0] = v.x, b.p[p][1] = v.y, b.p[p][2] = v.z, b.p[p][3] = v.w;
+              }
+            } else {
+              b = load_acts<XP>(xrow[n] + c * kChunk + seg * kSeg + 8 * j);
+            }
 #pragma unroll
             for (int p = 0; p < XP; ++p)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float (&to)[4] = part[p > 0][h][n];
-                mma(to, e[2 * h][0], e[2 * h + 1][0], e[2 * h][1], e[2 * h + 1][1], b.p[p][0], b.p[p][1]);
-                mma(to, e[2 * h][2], e[2 * h + 1][2], e[2 * h][3], e[2 * h + 1][3], b.p[p][2], b.p[p][3]);
+              for (int d = 0; d < 2; ++d) {              // the word's two MMAs
+                const int q = XP == 1 ? d : p > 0;
+                const bool opens = seg * kSeg % G == 0 && j == 0 && (XP == 1 || (d == 0 && p < 2));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  if (opens)
+                    mma_bf16_from0(part[q][h][n], e[2 * h][2 * d], e[2 * h + 1][2 * d], e[2 * h][2 * d + 1],
+                                   e[2 * h + 1][2 * d + 1], b.p[p][2 * d], b.p[p][2 * d + 1]);
+                  else
+                    mma_bf16(part[q][h][n], e[2 * h][2 * d], e[2 * h + 1][2 * d], e[2 * h][2 * d + 1],
+                             e[2 * h + 1][2 * d + 1], b.p[p][2 * d], b.p[p][2 * d + 1]);
+                }
               }
           }
         }
         if ((seg + 1) * kSeg % G == 0) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float s0 = __shfl_sync(0xffffffffu, rg.s[grp], g + 16 * h);
-            const float s1 = __shfl_sync(0xffffffffu, rg.s[grp], g + 16 * h + 8);
+            const float s0 = __shfl_sync(0xffffffffu, rg.s[grp], rho + 16 * h);
+            const float s1 = __shfl_sync(0xffffffffu, rg.s[grp], rho + 16 * h + 8);
 #pragma unroll
-            for (int q = XP > 1 ? 1 : 0; q >= 0; --q)
+            for (int q = 1; q >= 0; --q)
 #pragma unroll
               for (int n = 0; n < MT; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 4; ++j)
                   acc[h][n][j] = fmaf(j < 2 ? s0 : s1, part[q][h][n][j], acc[h][n][j]);
-                  part[q][h][n][j] = 0.f;
-                }
           }
         }
       }
-      stage = stage == kStages - 1 ? 0 : stage + 1;
+      ring.done();
     }
-    // ---- the band's sums: over the WK warps, then over the cluster
-    float* mine = red + warp * kRed;
+    float y[8 * MT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int n = 0; n < MT; ++n) {
+      float v[8];
+      turn_tile(tile, acc[0][n], acc[1][n], rho, t, lane, v);
 #pragma unroll
-      for (int n = 0; n < MT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mine[(n * 8 + 2 * t + (j & 1)) * 33 + 16 * h + g + (j >> 1) * 8] = acc[h][n][j];
-    if (sh.KC > 1)
-      cluster_sync();
-    else
-      __syncthreads();
-    const int cols = min(8 * MT, a.M - m0);
-    for (int x = threadIdx.x + kc * blockDim.x; x < sh.WR * 32 * cols; x += blockDim.x * sh.KC) {
-      const int row = x % 32, band = x / 32 % sh.WR, col = x / 32 / sh.WR;
-      const int n = (tile * sh.WR + band) * 32 + row;
-      const float* at = red + band * sh.WK * kRed + col * 33 + row;
-      float v = 0.f;
-      if (sh.KC == 1) {
-        for (int k = 0; k < sh.WK; ++k) v += at[k * kRed];
-      } else {
-        for (int r = 0; r < sh.KC; ++r) {
-          const uint32_t far = map_shared_rank(smem_u32(at), r);
-          for (int k = 0; k < sh.WK; ++k) {
-            float f;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(far + k * kRed * 4) : "memory");
-            v += f;
-          }
-        }
-      }
-      if (n < a.N) {
-        if (a.bias) v += a.bias[n];
-        const int64_t o = static_cast<int64_t>(m0 + col) * a.ldy + n;
-        if (a.ydt == QVLA_DTYPE_F32)
-          static_cast<float*>(a.y)[o] = v;
-        else
-          static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
-      }
+      for (int q = 0; q < 8; ++q) y[n * 8 + q] = v[q];
     }
-    // the partial sums may be overwritten (or their CTA leave) after this
-    if (sh.KC > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+    finish_band(a, sh, w, band, warp, lane, m0, cols, y, reinterpret_cast<float*>(smem + at.red),
+                reinterpret_cast<float*>(smem + at.far));
   }
+  ring.close(lane, err);
 }
 
-// Warps, bands and cluster of a launch, from N and K alone, so that a row's
-// result does not depend on the batch.  The model: an SM moves a 4 KB chunk in
-// about 90 ns, a warp needs about 1 us for its first chunk and 0.25 us for
-// each further one, a cluster's exchange costs about 1 us.
+// ============================================================== launches
+// Warps, bands and cluster of a launch, from N and K alone (a row's result
+// then depends on M only as far as the kernel does).  K is split as far as it
+// takes to give every one of 16 warps per SM a piece, first over the warps of a
+// CTA (exchange within its shared memory), then over a cluster's CTAs.  Against
+// the best of all splits with powers of two this was at most 8 % slower at
+// twelve sizes from 256 -> 256 to 2048 -> 131072.
 GemvShape gemv_shape(int N, int K, int sms) {
-  const int chunks = (K + kChunk - 1) / kChunk;
-  GemvShape best = {1, 1, 1};
-  double best_t = 1e30;
-  for (int KC = 1; KC <= 8; KC *= 2)
-    for (int WK = 1; WK <= 8; WK *= 2)
-      for (int WR = 1; WR * WK <= kMaxWarps; WR *= 2) {
-        if (KC * WK > chunks && KC * WK > 1) continue;
-        const int W = WR * WK;
-        if (W < 4 && chunks >= 4) continue;
-        const int64_t ctas = static_cast<int64_t>((N + 32 * WR - 1) / (32 * WR)) * KC;
-        const int64_t slots = static_cast<int64_t>(sms) * (16 / W);
-        if (KC > 1 && ctas > slots) continue;
-        const int64_t each = (chunks + KC * WK - 1) / (KC * WK);      // chunks of a warp and band
-        const double passes = static_cast<double>((ctas + slots - 1) / slots);
-        const double busy = static_cast<double>((ctas + sms - 1) / sms) * W * each * 0.09;
-        const double wait = 1.0 + 0.25 * (passes * each - 1) + 0.2 * passes + (KC > 1 ? 1.0 : 0.0);
-        const double time = (busy > wait ? busy : wait) + 0.05 * passes + 0.01 * WK;
-        if (time < best_t) {
-          best_t = time;
-          best = {WR, WK, KC};
-        }
-      }
-  return best;
+  const int bands = (N + 31) / 32, chunks = (K + kChunk - 1) / kChunk;
+  int split = 1;
+  while (2 * split <= chunks && 2 * split * bands <= 16 * sms) split *= 2;
+  GemvShape s = {};
+  s.WK = std::min(split, 8);
+  s.KC = std::min(split / s.WK, 8);
+  // eight warps a CTA; sixteen where a band has one or eight and there are bands enough
+  s.WR = s.KC > 1 ? 1 : std::max(1, (s.WK == 1 || s.WK == 8 ? 16 : 8) / s.WK);
+  while (s.WR > 1 && (s.WR - 1) * sms / 2 >= bands) s.WR /= 2;
+  s.stages = kStages;
+  return s;
 }
 
 int sm_count() {
@@ -466,26 +925,35 @@ int sm_count() {
   return n;
 }
 
-template <int G, int MT, int XP>
-cudaError_t run_gemv(const GemvArgs& a, cudaStream_t stream) {
-  auto kernel = gemv_kernel<G, MT, XP>;
-  constexpr int most = kMaxWarps * (kStages * kStageBytes + 8 * MT * 33 * 4);
-  static std::atomic<unsigned long long> done{0};
+// CTAs of an SM: what its shared memory and 512 threads of 128 registers hold.
+int resident_ctas(const GemvShape& sh, uint32_t smem) {
+  return std::max(1, std::min(227 * 1024 / static_cast<int>(smem + 2048), kMaxWarps / (sh.WR * sh.WK)));
+}
+
+int64_t wanted_ctas(const GemvShape& sh, int N) {
+  return static_cast<int64_t>(((N + 31) / 32 + sh.WR - 1) / sh.WR) * sh.KC;
+}
+
+template <typename K>
+cudaError_t launch_gemv(K kernel, std::atomic<unsigned long long>& done, const GemvArgs& a, const GemvShape& sh,
+                        uint32_t smem, int sms, cudaStream_t stream) {
   cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   });
   if (e != cudaSuccess) return e;
-  const int sms = sm_count();
-  if (sms == 0) return cudaErrorUnknown;
-  const GemvShape sh = gemv_shape(a.N, a.K, sms);
-  const int W = sh.WR * sh.WK;
-  const int64_t tiles = (a.N + 32 * sh.WR - 1) / (32 * sh.WR);
-  const int64_t slots = static_cast<int64_t>(sms) * (16 / W);
+  CUtensorMap codes;
+  if (!encode_map_2d(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq, a.K / 2, a.N, a.K / 2, kChunk / 2, 32,
+                     CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  unsigned int* err = device_error_word();
+  if (!err) return cudaErrorUnknown;
+  const int64_t ctas = wanted_ctas(sh, a.N);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * sh.KC <= slots ? tiles * sh.KC : slots),
-                     (a.M + 8 * MT - 1) / (8 * MT));
-  cfg.blockDim = dim3(32 * W);
-  cfg.dynamicSmemBytes = W * (kStages * kStageBytes + 8 * MT * 33 * 4);
+  cfg.gridDim = dim3(static_cast<unsigned>(
+                         sh.KC > 1 ? ctas : std::min<int64_t>(ctas, sms * resident_ctas(sh, smem))),
+                     (a.M + sh.rows - 1) / sh.rows);
+  cfg.blockDim = dim3(32 * sh.WR * sh.WK);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   int n = 0;
@@ -502,15 +970,81 @@ cudaError_t run_gemv(const GemvArgs& a, cudaStream_t stream) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kernel, a, sh);
+  return cudaLaunchKernelEx(&cfg, kernel, a, sh, codes, err);
+}
+
+// Gives up ring stages, then bands at a time (neither changes a result), until
+// `bytes` of shared memory fit; then the third stage, where without it more
+// CTAs are on an SM at once and there are CTAs for them (16384 -> 2048, one
+// row: 8.1 against 13.5 us).
+template <typename F>
+bool make_fit(GemvShape& sh, int N, int sms, F bytes) {
+  while (bytes(sh) > kMaxSmem) {
+    if (sh.stages > 2)
+      --sh.stages;
+    else if (sh.WR > 1)
+      sh.WR /= 2;
+    else
+      return false;
+  }
+  if (sh.stages > 2) {
+    GemvShape two = sh;
+    two.stages = 2;
+    const int now = resident_ctas(sh, bytes(sh));
+    if (resident_ctas(two, bytes(two)) > now && wanted_ctas(sh, N) > static_cast<int64_t>(now) * sms) sh = two;
+  }
+  return true;
+}
+
+template <int G, int ND, bool ZERO>
+cudaError_t run_planes(const GemvArgs& a, GemvShape sh, int sms, cudaStream_t stream) {
+  auto bytes = [&](const GemvShape& s) { return plane_layout(s, a.K, G, ND, ZERO).bytes; };
+  sh.rows = a.M;
+  const GemvShape whole = sh;
+  if (!make_fit(sh, a.N, sms, bytes)) {                  // two rows of the largest K: one pass each
+    sh = whole;
+    sh.rows = 1;
+    while (!make_fit(sh, a.N, sms, bytes)) sh.WK /= 2;   // and with the finest groups fewer warps
+  }
+  static std::atomic<unsigned long long> done{0};
+  return launch_gemv(gemv_planes_kernel<G, ND, ZERO>, done, a, sh, bytes(sh), sms, stream);
+}
+
+template <int G, int MT, int XP>
+cudaError_t run_parts(const GemvArgs& a, GemvShape sh, int sms, cudaStream_t stream) {
+  sh.rows = std::min(a.M, 8 * MT);
+  // Operand order is worth its staging where warps take several bands
+  // (2048 -> 131072, 16 rows: 53.6 against 60.8 us) or the activations have to
+  // be split (1536 -> 6144, seven fp32 rows: 8.6 against 9.8 us), and the
+  // activations leave room for rings of two stages.
+  GemvShape st = sh;
+  if (sh.KC == 1 && (XP > 1 || wanted_ctas(sh, a.N) > sms)) {
+    auto bytes = [&](const GemvShape& s) { return part_layout(s, a.K, XP, true).bytes; };
+    while (st.stages > 2 && bytes(st) > kMaxSmem) --st.stages;
+    if (bytes(st) <= kMaxSmem) {
+      make_fit(st, a.N, sms, bytes);
+      static std::atomic<unsigned long long> done{0};
+      return launch_gemv(gemv_parts_kernel<G, MT, XP, true>, done, a, st, bytes(st), sms, stream);
+    }
+  }
+  auto bytes = [&](const GemvShape& s) { return part_layout(s, a.K, XP, false).bytes; };
+  if (!make_fit(sh, a.N, sms, bytes)) return cudaErrorInvalidValue;
+  static std::atomic<unsigned long long> done{0};
+  return launch_gemv(gemv_parts_kernel<G, MT, XP, false>, done, a, sh, bytes(sh), sms, stream);
 }
 
 template <int G>
 cudaError_t run_group(const GemvArgs& a, cudaStream_t stream) {
-  if (a.xdt == QVLA_DTYPE_F32)
-    return a.M <= 8 ? run_gemv<G, 1, 3>(a, stream) : run_gemv<G, 2, 3>(a, stream);
-  if (a.M <= 8) return run_gemv<G, 1, 1>(a, stream);
-  return a.M <= 16 ? run_gemv<G, 2, 1>(a, stream) : run_gemv<G, 4, 1>(a, stream);
+  const int sms = sm_count();
+  if (sms == 0) return cudaErrorUnknown;
+  const GemvShape sh = gemv_shape(a.N, a.K, sms);
+  const bool f32 = a.xdt == QVLA_DTYPE_F32;
+  if (a.M <= 2) {
+    if (f32) return a.zero ? run_planes<G, 4, true>(a, sh, sms, stream) : run_planes<G, 4, false>(a, sh, sms, stream);
+    return a.zero ? run_planes<G, 3, true>(a, sh, sms, stream) : run_planes<G, 3, false>(a, sh, sms, stream);
+  }
+  if (f32) return a.M <= 8 ? run_parts<G, 1, 3>(a, sh, sms, stream) : run_parts<G, 2, 3>(a, sh, sms, stream);
+  return a.M <= 8 ? run_parts<G, 1, 1>(a, sh, sms, stream) : run_parts<G, 2, 1>(a, sh, sms, stream);
 }
 
 }  // namespace
