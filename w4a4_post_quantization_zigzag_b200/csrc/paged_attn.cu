@@ -115,23 +115,37 @@ QVLA_DEVICE Span span_of(const PagedAttnArgs& a, int b) {
   return {static_cast<int>(seen), static_cast<int>(n - seen)};
 }
 
+// The line's length T cut into equal pieces, one per warp of as many CTAs as
+// there is length for: the first `more` pieces have length each + 1.
+struct Cut {
+  int ctas;
+  int64_t each, more;
+  int warps;
+  QVLA_DEVICE Cut(int64_t T, int W) : warps(W) {
+    ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (T + 2 * W - 1) / (2 * W)));
+    const int pieces = max(ctas, 1) * W;
+    each = T < (1ll << 31) ? static_cast<int>(T) / pieces : T / pieces;
+    more = T - each * pieces;
+  }
+  QVLA_DEVICE int64_t start(int piece) const { return each * piece + min(static_cast<int64_t>(piece), more); }
+  // the CTA whose pieces hold place x
+  QVLA_DEVICE int owner(int64_t x) const {
+    const int64_t big = more * (each + 1);
+    const int64_t piece = x < big ? x / (each + 1) : more + (x - big) / each;
+    return static_cast<int>(piece / warps);
+  }
+};
+
 struct Cursor {
   int b, hu, tile, tiles;
   Span s;
+  template <int TK>
   QVLA_DEVICE void seek(const PagedAttnArgs& a) {      // first sequence from b on with tokens
     for (; b < a.B; ++b) {
       s = span_of(a, b);
-      tiles = (s.visible + 15) / 16;
+      tiles = (s.visible + TK - 1) / TK;
       if (tiles) return;
     }
-  }
-  QVLA_DEVICE void next(const PagedAttnArgs& a, int HU) {
-    if (++tile < tiles) return;
-    tile = 0;
-    if (++hu < HU) return;
-    hu = 0;
-    ++b;
-    seek(a);
   }
 };
 
@@ -160,15 +174,6 @@ __host__ __device__ Scratch scratch_at(void* ws) {
 }
 
 template <typename X>
-QVLA_DEVICE void store_out(const PagedAttnArgs& a, int b, int h, int d, float v) {
-  X* p = static_cast<X*>(a.out) + b * a.ldo + static_cast<int64_t>(h) * a.cache.dim + d;
-  if constexpr (sizeof(X) == 2)
-    *p = __float2bfloat16_rn(v);
-  else
-    *p = v;
-}
-
-template <typename X>
 QVLA_DEVICE void store_out4(const PagedAttnArgs& a, int b, int h, int d, float4 v) {
   X* p = static_cast<X*>(a.out) + b * a.ldo + static_cast<int64_t>(h) * a.cache.dim + d;
   if constexpr (sizeof(X) == 2)
@@ -187,44 +192,60 @@ QVLA_DEVICE float weight(float m, float M) { return m == -INFINITY ? 0.f : exp2_
 
 // DP: head dim rounded up; NT: columns of 8 query heads; QP: bf16 parts of q
 // and p (1 for bf16 q, 3 for fp32: their sum is the whole value); BITS of the
-// cache; W warps, S stages of one tile each per warp.
-template <int DP, int NT, int QP, int BITS, int W, int S>
+// cache; W warps, S stages of one tile of TK tokens per warp.
+template <int DP, int NT, int QP, int BITS, int W, int S, int TK>
 struct Shape {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kRow = DP * BITS / 8;               // bytes of a token's row
   static constexpr int kChunks = kRow / 16;
-  static constexpr int kTile = 16 * kRow;
-  static constexpr int kStage = 2 * kTile + (BITS == 8 ? 128 : 0);
+  static constexpr int kTile = TK * kRow;
+  static constexpr int kStage = 2 * kTile + (BITS == 8 ? 8 * TK : 0);
   static constexpr int kSmem = W * S * kStage;
   static_assert(S * kStage >= kHeads * DP * 4, "a warp's ring holds its last partial result");
+  static_assert(2 * W <= 32, "a lane for every partial result of a CTA");
 };
 
-template <typename X, int DP, int NT, int QP, int BITS, int W, int S>
+// 16-byte piece of a row in its tile: eight rows of one piece meet no bank twice.
+template <int kChunks>
+QVLA_DEVICE int piece_at(int row, int piece) {
+  return kChunks == 4 ? piece ^ (row >> 1 & 3) : piece ^ (row & 7);
+}
+
+template <typename X, int DP, int NT, int QP, int BITS, int W, int S, int TK>
 __global__ void __launch_bounds__(32 * W, 1)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, unsigned int* err) {
-  using Sh = Shape<DP, NT, QP, BITS, W, S>;
-  constexpr int kHeads = Sh::kHeads, kChunks = Sh::kChunks, kKs = DP / 16;
+  using Sh = Shape<DP, NT, QP, BITS, W, S, TK>;
+  constexpr int kHeads = Sh::kHeads, kChunks = Sh::kChunks, kKs = DP / 16, kSub = TK / 16;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ int4 meta[W][S];                 // {b, unit head, valid rows | begins << 16 | ends << 17, 0}
+  __shared__ int4 meta[W][S];                 // {b, unit head, rows that are there, flags} of each stage
   __shared__ int64_t scan[W];
-  __shared__ int64_t start_before[W];         // tiles of a head before the sequence
+  __shared__ int64_t start_before[W];         // length of a head's line before the sequence
   __shared__ int start_b[W];
-  __shared__ int4 slot[W][2];                 // {b (-1: empty), unit head, begins, ends}
-  __shared__ float2 slot_stat[W][2][kHeads];
+  __shared__ int4 slot[2 * W];                // partial results {b (-1: none), unit head, begins, ends}
+  __shared__ float2 slot_stat[2 * W][kHeads];
+  __shared__ float slot_weight[2 * W][kHeads];
+  __shared__ float2 unit_stat[2 * W][kHeads];
+  enum { kBegins = 1, kEnds = 2, kLast = 4 };
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int D = a.cache.dim, G = a.Hq / a.cache.heads;
   const int HT = (G + kHeads - 1) / kHeads, HU = a.cache.heads * HT;
   const Scratch ws = scratch_at<kHeads, DP>(a.ws);
-  if (threadIdx.x < 2 * W) (&slot[0][0])[threadIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x < 2 * W) slot[threadIdx.x] = make_int4(-1, 0, 0, 0);
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- the line: tiles of one head before each thread's share of sequences
+  // ---- the line: its length for one head before each thread's share of
+  // sequences.  A sequence takes a place per tile and one for its beginning
+  // (the query, the end of the unit before), which costs about as much.
+  auto length = [&](int b) {
+    const int n = (span_of(a, b).visible + TK - 1) / TK;
+    return n ? n + 1 : 0;
+  };
   const int per = (a.B + 32 * W - 1) / (32 * W);
   const int b_lo = min(static_cast<int>(threadIdx.x) * per, a.B), b_hi = min(b_lo + per, a.B);
   int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += (span_of(a, b).visible + 15) / 16;
+  for (int b = b_lo; b < b_hi; ++b) mine += length(b);
   int64_t upto = mine;
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
@@ -237,18 +258,16 @@ __global__ void __launch_bounds__(32 * W, 1)
     if (w < warp) before += scan[w];
     all += scan[w];
   }
-  const int64_t T = all * HU;
-  const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (T + W - 1) / W));
-  const int64_t pieces = static_cast<int64_t>(ctas) * W;
-  const bool works = static_cast<int>(blockIdx.x) < ctas;
+  const Cut cut(all * HU, W);
+  const bool works = static_cast<int>(blockIdx.x) < cut.ctas;
   if (works) {
     for (int w = 0; w < W; ++w) {
-      const int64_t x = (static_cast<int64_t>(blockIdx.x) * W + w) * T / pieces;
+      const int64_t x = cut.start(blockIdx.x * W + w);
       if (x >= before * HU && x < (before + mine) * HU) {
         int64_t at = before;
         int b = b_lo;
         for (;; ++b) {
-          const int64_t n = (span_of(a, b).visible + 15) / 16;
+          const int n = length(b);
           if (x < (at + n) * HU) break;
           at += n;
         }
@@ -261,76 +280,101 @@ __global__ void __launch_bounds__(32 * W, 1)
 
   int4 lead = make_int4(0, 0, 0, 0);
   if (works) {
-    const int64_t lo = (static_cast<int64_t>(blockIdx.x) * W + warp) * T / pieces;
-    const int64_t hi = (static_cast<int64_t>(blockIdx.x) * W + warp + 1) * T / pieces;
-    const int count = static_cast<int>(hi - lo);
+    const int64_t lo = cut.start(blockIdx.x * W + warp);
+    int64_t left = cut.start(blockIdx.x * W + warp + 1) - lo;        // places of this piece not fed yet
     const uint32_t ring0 = smem_u32(ring) + warp * S * Sh::kStage;
 
-    Cursor in;
-    in.b = count ? start_b[warp] : a.B;
-    in.hu = in.tile = in.tiles = 0;
-    if (count) {
+    Cursor in = {};
+    if (left > 0) {
+      in.b = start_b[warp];
       in.s = span_of(a, in.b);
-      in.tiles = (in.s.visible + 15) / 16;
+      in.tiles = (in.s.visible + TK - 1) / TK;
       const int64_t off = lo - start_before[warp] * HU;
-      in.hu = static_cast<int>(off / in.tiles);
-      in.tile = static_cast<int>(off - static_cast<int64_t>(in.hu) * in.tiles);
+      const int len = in.tiles + 1;
+      in.hu = off < (1ll << 31) ? static_cast<int>(off) / len : static_cast<int>(off / len);
+      const int r = static_cast<int>(off - static_cast<int64_t>(in.hu) * len);
+      in.tile = max(r - 1, 0);
+      if (r == 0) --left;
     }
 
-    // ---- feeding: the page of each row is read one tile ahead of its copy
-    int row_page = 0, row_tok = 0;
-    bool row_in = false;
-    auto look_up = [&] {
-      const int v = in.tile * 16 + (lane & 15);
-      row_in = v < in.s.visible;
-      const int t = row_in ? (v >= a.sinks ? v + in.s.gap : v) : 0;
-      const int p = t / a.cache.page_size;
-      row_tok = t - p * a.cache.page_size;
-      row_page = row_in ? a.page_table[static_cast<int64_t>(in.b) * a.max_pages + p] : 0;
+    // ---- feeding.  Two tiles' page numbers are read ahead of the copies.
+    struct Row {
+      bool valid, in;          // a tile; a row of it for this lane
+      int b, hu, flags, page, tok;
     };
-    auto feed = [&](int stage) {
-      const bool found = row_page >= 0 && row_page < a.cache.pages;
-      if (row_in && !found && lane < 16) report(err, QVLA_DEVERR_CACHE_RANGE);
-      const bool ok = row_in && found;
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      const int kh = in.hu / HT;
-      const int64_t off = ok ? row_page * a.cache.page_stride + row_tok * a.cache.token_stride +
+    auto look_up = [&]() -> Row {
+      Row r = {};
+      if (left <= 0) return r;
+      r.valid = true;
+      r.b = in.b;
+      r.hu = in.hu;
+      r.flags = (in.tile == 0 ? kBegins : 0) | (in.tile == in.tiles - 1 ? kEnds : 0);
+      const int v = in.tile * TK + (lane & (TK - 1));
+      r.in = v < in.s.visible;
+      if (r.in) {
+        const int t = v >= a.sinks ? v + in.s.gap : v;
+        const int p = t / a.cache.page_size;
+        r.tok = t - p * a.cache.page_size;
+        r.page = a.page_table[static_cast<int64_t>(in.b) * a.max_pages + p];
+      }
+      --left;
+      if (++in.tile == in.tiles) {
+        in.tile = 0;
+        --left;                // the next unit's beginning
+        if (++in.hu == HU) {
+          in.hu = 0;
+          ++in.b;
+          if (left > 0) in.template seek<TK>(a);
+        }
+      }
+      if (left <= 0) r.flags |= kLast;
+      return r;
+    };
+    auto feed = [&](const Row& r, int stage) {
+      const bool found = r.page >= 0 && r.page < a.cache.pages;
+      if (r.in && !found && lane < TK) report(err, QVLA_DEVERR_CACHE_RANGE);
+      const bool ok = r.in && found;
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      const int kh = r.hu / HT;
+      const int64_t off = ok ? r.page * a.cache.page_stride + r.tok * a.cache.token_stride +
                                    kh * a.cache.head_stride
                              : 0;
       const uint32_t dst0 = ring0 + stage * Sh::kStage;
-      const int chunk = lane % kChunks;
-      const bool col = chunk * (128 / BITS) < D;
+      const int piece = lane % kChunks;
+      const bool col = piece * (128 / BITS) < D;
 #pragma unroll
-      for (int i = 0; i < kChunks / 2; ++i) {
+      for (int i = 0; i < kChunks * TK / 32; ++i) {
         const int row = i * (32 / kChunks) + lane / kChunks;
-        const int64_t ro = __shfl_sync(0xffffffffu, off, row) * (BITS / 8) + chunk * 16;
+        const int64_t ro = __shfl_sync(0xffffffffu, off, row) * (BITS / 8) + piece * 16;
         const bool take = col && (mask >> row & 1);
-        const int phys = kChunks == 4 ? chunk ^ (row >> 1 & 3) : chunk ^ (row & 7);
-        const uint32_t dst = dst0 + row * Sh::kRow + phys * 16;
+        const uint32_t dst = dst0 + row * Sh::kRow + piece_at<kChunks>(row, piece) * 16;
         cp_async16(dst, static_cast<const uint8_t*>(a.cache.k) + (take ? ro : 0), take);
         cp_async16(dst + Sh::kTile, static_cast<const uint8_t*>(a.cache.v) + (take ? ro : 0), take);
       }
       if constexpr (BITS == 8) {
-        const int64_t so = ok ? row_page * a.cache.s_page_stride + row_tok * a.cache.s_token_stride +
+        const int64_t so = ok ? r.page * a.cache.s_page_stride + r.tok * a.cache.s_token_stride +
                                     kh * a.cache.s_head_stride
                               : 0;
-        cp_async4(dst0 + 2 * Sh::kTile + lane * 4, (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + so, ok);
+        const uint32_t to = dst0 + 2 * Sh::kTile + lane * 4;
+        if constexpr (TK == 32) {
+          cp_async4(to, a.cache.k_scale + so, ok);
+          cp_async4(to + 128, a.cache.v_scale + so, ok);
+        } else {
+          cp_async4(to, (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + so, ok);
+        }
       }
-      if (lane == 0)
-        meta[warp][stage] = make_int4(in.b, in.hu, static_cast<int>(mask) | (in.tile == 0) << 16 |
-                                                       (in.tile == in.tiles - 1) << 17, 0);
+      if (lane == 0) meta[warp][stage] = make_int4(r.b, r.hu, static_cast<int>(mask), r.flags);
     };
 
     int fed = 0;
-    if (count) look_up();
+    Row now = look_up(), then = look_up();
 #pragma unroll 1
     for (int s = 0; s < S - 1; ++s) {
-      if (fed < count) {
-        feed(s);
-        if (++fed < count) {
-          in.next(a, HU);
-          look_up();
-        }
+      if (now.valid) {
+        feed(now, s);
+        ++fed;
+        now = then;
+        then = look_up();
       }
       cp_async_commit();
     }
@@ -344,23 +388,14 @@ __global__ void __launch_bounds__(32 * W, 1)
     bool fresh = true, begun = false;
     int stage = 0;
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      cp_async_wait<S - 2>();
+    for (int i = 0; i < fed; ++i) {
       __syncwarp();
       const int4 mt = meta[warp][stage];
-      if (fed < count) {
-        feed(stage == 0 ? S - 1 : stage - 1);
-        if (++fed < count) {
-          in.next(a, HU);
-          look_up();
-        }
-      }
-      cp_async_commit();
-
       const int kh = mt.y / HT, h0 = mt.y % HT * kHeads;         // first head within the group
       if (fresh) {
+        // the columns of Q^T of the unit, in registers, while its first tile comes
         fresh = false;
-        begun = mt.z >> 16 & 1;
+        begun = mt.w & kBegins;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const bool in_group = h0 + n * 8 + g < G;
@@ -407,50 +442,58 @@ __global__ void __launch_bounds__(32 * W, 1)
           for (int k = 0; k < kKs; ++k) o[k][n][0] = o[k][n][1] = o[k][n][2] = o[k][n][3] = 0.f;
         }
       }
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      if (now.valid) {
+        feed(now, stage == 0 ? S - 1 : stage - 1);
+        ++fed;
+        now = then;
+        then = look_up();
+      }
+      cp_async_commit();
 
       const uint32_t kt = ring0 + stage * Sh::kStage, vt = kt + Sh::kTile;
+      const int row = lane & 15;
       // S^T = K Q^T, two chains of sums
-      float c[NT][4];
+      float c[kSub][NT][4];
       auto scores = [&](auto parts) {
-        float c2[2][NT][4] = {};
-        if constexpr (BITS == 16) {
-          const int row = lane & 15;
-          const uint32_t base = kt + row * Sh::kRow;
 #pragma unroll
-          for (int k = 0; k < kKs; ++k) {
-            uint32_t f[4];
-            ldsm4(base + ((2 * k + (lane >> 4)) ^ (row & 7)) * 16, f);
+        for (int u = 0; u < kSub; ++u) {
+          float c2[2][NT][4] = {};
+          const uint32_t base = kt + (u * 16 + row) * Sh::kRow;
+          if constexpr (BITS == 16) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int p = 0; p < decltype(parts)::value; ++p)
-                mma(c2[k & 1][n], f[0], f[1], f[2], f[3], qf[p][n][k][0], qf[p][n][k][1]);
-          }
-        } else {
-          const int row = lane & 15;
-          const uint32_t base = kt + row * Sh::kRow;
-#pragma unroll
-          for (int k = 0; k < kKs; k += 2) {
-            const int chunk = k + (lane >> 4);
-            const int phys = kChunks == 4 ? chunk ^ (row >> 1 & 3) : chunk ^ (row & 7);
-            uint32_t f[4];
-            ldsm4(base + phys * 16, f);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t a0 = codes2(f[2 * j]), a1 = codes2(f[2 * j + 1]);
-              const uint32_t a2 = codes2(f[2 * j] >> 8), a3 = codes2(f[2 * j + 1] >> 8);
+            for (int k = 0; k < kKs; ++k) {
+              uint32_t f[4];
+              ldsm4(base + piece_at<kChunks>(row, 2 * k + (lane >> 4)) * 16, f);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int p = 0; p < decltype(parts)::value; ++p)
-                  mma(c2[j][n], a0, a1, a2, a3, qf[p][n][k + j][0], qf[p][n][k + j][1]);
+                  mma(c2[k & 1][n], f[0], f[1], f[2], f[3], qf[p][n][k][0], qf[p][n][k][1]);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kKs; k += 2) {
+              uint32_t f[4];
+              ldsm4(base + piece_at<kChunks>(row, k + (lane >> 4)) * 16, f);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t a0 = codes2(f[2 * j]), a1 = codes2(f[2 * j + 1]);
+                const uint32_t a2 = codes2(f[2 * j] >> 8), a3 = codes2(f[2 * j + 1] >> 8);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int p = 0; p < decltype(parts)::value; ++p)
+                    mma(c2[j][n], a0, a1, a2, a3, qf[p][n][k + j][0], qf[p][n][k + j][1]);
+              }
             }
           }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[u][n][j] = c2[0][n][j] + c2[1][n][j];
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) c[n][j] = c2[0][n][j] + c2[1][n][j];
       };
       scores(std::integral_constant<int, QP>());
       if constexpr (QP > 1) {
@@ -458,43 +501,57 @@ __global__ void __launch_bounds__(32 * W, 1)
         // first part alone (which has its sign) gives the score
         bool nan = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) nan |= c[n][j] != c[n][j];
-        if (__any_sync(0xffffffffu, nan)) {
-          float whole[NT][4];
+        for (int u = 0; u < kSub; ++u)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) whole[n][j] = c[n][j];
+            for (int j = 0; j < 4; ++j) nan |= c[u][n][j] != c[u][n][j];
+        if (__any_sync(0xffffffffu, nan)) {
+          float whole[kSub][NT][4];
+#pragma unroll
+          for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) whole[u][n][j] = c[u][n][j];
           scores(std::integral_constant<int, 1>());
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int u = 0; u < kSub; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (whole[n][j] == whole[n][j]) c[n][j] = whole[n][j];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (whole[u][n][j] == whole[u][n][j]) c[u][n][j] = whole[u][n][j];
         }
       }
 
       // scale, leave out rows that are not there
-      float ks0 = sc, ks1 = sc, vs0 = 1.f, vs1 = 1.f;
-      if constexpr (BITS == 8) {
-        const float* sp = reinterpret_cast<const float*>(ring + (kt - smem_u32(ring)) + 2 * Sh::kTile);
-        ks0 *= sp[g];
-        ks1 *= sp[g + 8];
-        vs0 = sp[16 + g];
-        vs1 = sp[24 + g];
-      }
-      const bool in0 = mt.z >> g & 1, in1 = mt.z >> (g + 8) & 1;
+      float vs[kSub][2];
+#pragma unroll
+      for (int u = 0; u < kSub; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float ks = sc;
+          const int at = u * 16 + g + 8 * r;
+          if constexpr (BITS == 8) {
+            const float* sp = reinterpret_cast<const float*>(ring + (kt - smem_u32(ring)) + 2 * Sh::kTile);
+            ks *= sp[at];
+            vs[u][r] = sp[TK + at];
+          }
+          const bool there = mt.z >> at & 1;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) c[u][n][2 * r + j] = there ? c[u][n][2 * r + j] * ks : -INFINITY;
+        }
       bool grew = false;
       float mn[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          c[n][j] = in0 ? c[n][j] * ks0 : -INFINITY;
-          c[n][j + 2] = in1 ? c[n][j + 2] * ks1 : -INFINITY;
-          float x = fmaxf(c[n][j], c[n][j + 2]);
+          float x = fmaxf(c[0][n][j], c[0][n][j + 2]);
+          if constexpr (kSub > 1) x = fmaxf(x, fmaxf(c[kSub - 1][n][j], c[kSub - 1][n][j + 2]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -516,70 +573,71 @@ __global__ void __launch_bounds__(32 * W, 1)
             }
           }
       }
-      uint32_t pf[QP][NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int u = 0; u < kSub; ++u) {
+        uint32_t pf[QP][NT][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float base = m[n][j] == -INFINITY ? 0.f : m[n][j];
-          c[n][j] = exp2_fast(c[n][j] - base);
-          c[n][j + 2] = exp2_fast(c[n][j + 2] - base);
-          l[n][j] += c[n][j] + c[n][j + 2];
-          if constexpr (BITS == 8) {
-            c[n][j] *= vs0;
-            c[n][j + 2] *= vs1;
-          }
-        }
-        // tokens to the rows of the second product's right operand; bf16 q
-        // rounds p to its own precision, fp32 q takes p whole
-        if constexpr (QP == 1) {
-          pf[0][n][0] = movm_t(pack2(c[n][0], c[n][1]));
-          pf[0][n][1] = movm_t(pack2(c[n][2], c[n][3]));
-        } else {
-#pragma unroll
-          for (int p = 0; p < QP; ++p) {
-            pf[p][n][0] = movm_t(take2(c[n][0], c[n][1]));
-            pf[p][n][1] = movm_t(take2(c[n][2], c[n][3]));
-          }
-        }
-      }
-      // O^T += V^T P^T
-      if constexpr (BITS == 16) {
-        // matrices: tokens 0-7 and 8-15 of values 0-7, then of values 8-15
-        const int row = (lane & 7) + (lane >> 4 & 1) * 8;
-        const uint32_t base = vt + row * Sh::kRow;
-#pragma unroll
-        for (int k = 0; k < kKs; ++k) {
-          uint32_t f[4];
-          ldsm4_t(base + ((2 * k + (lane >> 3 & 1)) ^ (row & 7)) * 16, f);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int p = 0; p < QP; ++p) mma(o[k][n], f[0], f[1], f[2], f[3], pf[p][n][0], pf[p][n][1]);
-        }
-      } else {
-        const int row = lane & 15;
-        const uint32_t base = vt + row * Sh::kRow;
-#pragma unroll
-        for (int k = 0; k < kKs; k += 2) {
-          const int chunk = k + (lane >> 4);
-          const int phys = kChunks == 4 ? chunk ^ (row >> 1 & 3) : chunk ^ (row & 7);
-          uint32_t f[4];
-          ldsm4_t(base + phys * 16, f);
+        for (int n = 0; n < NT; ++n) {
+          float* x = c[u][n];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t a0 = codes2(f[2 * j]), a1 = codes2(f[2 * j] >> 8);
-            const uint32_t a2 = codes2(f[2 * j + 1]), a3 = codes2(f[2 * j + 1] >> 8);
+            const float base = m[n][j] == -INFINITY ? 0.f : m[n][j];
+            x[j] = exp2_fast(x[j] - base);
+            x[j + 2] = exp2_fast(x[j + 2] - base);
+            l[n][j] += x[j] + x[j + 2];
+            if constexpr (BITS == 8) {
+              x[j] *= vs[u][0];
+              x[j + 2] *= vs[u][1];
+            }
+          }
+          // tokens to the rows of the second product's right operand; bf16 q
+          // rounds p to its own precision, fp32 q takes p whole
+          if constexpr (QP == 1) {
+            pf[0][n][0] = movm_t(pack2(x[0], x[1]));
+            pf[0][n][1] = movm_t(pack2(x[2], x[3]));
+          } else {
+#pragma unroll
+            for (int p = 0; p < QP; ++p) {
+              pf[p][n][0] = movm_t(take2(x[0], x[1]));
+              pf[p][n][1] = movm_t(take2(x[2], x[3]));
+            }
+          }
+        }
+        // O^T += V^T P^T
+        if constexpr (BITS == 16) {
+          // matrices: tokens 0-7 and 8-15 of values 0-7, then of values 8-15
+          const int vrow = (lane & 7) + (lane >> 4 & 1) * 8;
+          const uint32_t base = vt + (u * 16 + vrow) * Sh::kRow;
+#pragma unroll
+          for (int k = 0; k < kKs; ++k) {
+            uint32_t f[4];
+            ldsm4_t(base + piece_at<kChunks>(vrow, 2 * k + (lane >> 3 & 1)) * 16, f);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int p = 0; p < QP; ++p) mma(o[k + j][n], a0, a1, a2, a3, pf[p][n][0], pf[p][n][1]);
+              for (int p = 0; p < QP; ++p) mma(o[k][n], f[0], f[1], f[2], f[3], pf[p][n][0], pf[p][n][1]);
+          }
+        } else {
+          const uint32_t base = vt + (u * 16 + row) * Sh::kRow;
+#pragma unroll
+          for (int k = 0; k < kKs; k += 2) {
+            uint32_t f[4];
+            ldsm4_t(base + piece_at<kChunks>(row, k + (lane >> 4)) * 16, f);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t a0 = codes2(f[2 * j]), a1 = codes2(f[2 * j] >> 8);
+              const uint32_t a2 = codes2(f[2 * j + 1]), a3 = codes2(f[2 * j + 1] >> 8);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int p = 0; p < QP; ++p) mma(o[k + j][n], a0, a1, a2, a3, pf[p][n][0], pf[p][n][1]);
+            }
           }
         }
       }
 
       // ---- the unit, or this warp's piece of the line, ends here
-      const bool ends = mt.z >> 17 & 1, last = i == count - 1;
+      const bool ends = mt.w & kEnds, last = mt.w & kLast;
       if (ends || last) {
         fresh = true;
 #pragma unroll
@@ -587,129 +645,144 @@ __global__ void __launch_bounds__(32 * W, 1)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             for (int d = 4; d < 32; d <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], d);
-        if (last) {
-          // every copy has landed and every lane has read its last tile: the
-          // ring is free for the partial result
-          cp_async_wait<0>();
-          __syncwarp();
-        }
-        const bool whole = begun && ends;
-        float* dst = last ? reinterpret_cast<float*>(ring + warp * S * Sh::kStage)
-                          : ws.warp_o + (static_cast<size_t>(blockIdx.x) * W + warp) * kHeads * DP;
+        if (begun && ends && !last) {
+          // the whole unit was this warp's: its result, from the registers
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int h = n * 8 + 2 * t4 + j;
-            const bool in_group = h0 + h < G;
-            const int hq = kh * G + h0 + h;
-            const float scale_o = whole ? (l[n][j] == 0.f ? 0.f : 1.f / l[n][j]) : 1.f;
+            for (int j = 0; j < 2; ++j) {
+              const int h = h0 + n * 8 + 2 * t4 + j;
+              if (h >= G) continue;
+              const bool none = l[n][j] == 0.f;            // an empty sum stays 0 whatever the values were
+              const float r = none ? 0.f : 1.f / l[n][j];
+              X* to = static_cast<X*>(a.out) + mt.x * a.ldo + static_cast<int64_t>(kh * G + h) * D +
+                      (BITS == 8 ? 2 * g : g);
 #pragma unroll
-            for (int k = 0; k < kKs; ++k) {
-              const int d0 = k * 16 + (BITS == 8 ? 2 * g : g), d1 = BITS == 8 ? d0 + 1 : d0 + 8;
-              // an empty sum stays 0 whatever the values were
-              const float v0 = whole && l[n][j] == 0.f ? 0.f : o[k][n][j] * scale_o;
-              const float v1 = whole && l[n][j] == 0.f ? 0.f : o[k][n][j + 2] * scale_o;
-              if (whole) {
-                if (in_group && k * 16 < D) {
-                  store_out<X>(a, mt.x, hq, d0, v0);
-                  store_out<X>(a, mt.x, hq, d1, v1);
+              for (int k = 0; k < kKs; ++k) {
+                const float v0 = none ? 0.f : o[k][n][j] * r, v1 = none ? 0.f : o[k][n][j + 2] * r;
+                if (k * 16 >= D) continue;
+                if constexpr (sizeof(X) == 2) {
+                  to[k * 16] = __float2bfloat16_rn(v0);
+                  to[k * 16 + (BITS == 8 ? 1 : 8)] = __float2bfloat16_rn(v1);
+                } else {
+                  to[k * 16] = v0;
+                  to[k * 16 + (BITS == 8 ? 1 : 8)] = v1;
                 }
-              } else {
-                dst[h * DP + d0] = v0;
-                dst[h * DP + d1] = v1;
               }
+              if (a.lse && g == 0) a.lse[static_cast<int64_t>(mt.x) * a.Hq + kh * G + h] = lse_of(m[n][j], l[n][j]);
             }
-            if (g == 0) {
-              if (whole) {
-                if (a.lse && in_group) a.lse[static_cast<int64_t>(mt.x) * a.Hq + hq] = lse_of(m[n][j], l[n][j]);
-              } else {
-                slot_stat[warp][last][h] = make_float2(m[n][j], l[n][j]);
+        } else {
+          // a part: in the warp's ring after its last tile (every copy has
+          // landed, every lane has read), else in its place in the scratch
+          __syncwarp();
+          float* to = (last ? reinterpret_cast<float*>(ring + warp * S * Sh::kStage)
+                            : ws.warp_o + (static_cast<size_t>(blockIdx.x) * W + warp) * kHeads * DP) +
+                      2 * t4 * DP + (BITS == 8 ? 2 * g : g);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+              for (int k = 0; k < kKs; ++k) {
+                to[(n * 8 + j) * DP + k * 16] = o[k][n][j];
+                to[(n * 8 + j) * DP + k * 16 + (BITS == 8 ? 1 : 8)] = o[k][n][j + 2];
               }
+              if (g == 0) slot_stat[2 * warp + last][n * 8 + 2 * t4 + j] = make_float2(m[n][j], l[n][j]);
             }
-          }
-        if (!whole && lane == 0) slot[warp][last] = make_int4(mt.x, mt.y, begun, ends);
+          if (lane == 0) slot[2 * warp + last] = make_int4(mt.x, mt.y, begun, ends);
+        }
       }
       stage = stage == S - 1 ? 0 : stage + 1;
     }
     cp_async_wait<0>();
     __syncthreads();
 
-    // ---- join the CTA's partial results, unit by unit in the line's order
-    const int4* sl = &slot[0][0];
-    for (int i = 0; i < 2 * W;) {
-      const int4 u = sl[i];
-      if (u.x < 0) {
-        ++i;
-        continue;
+    // ---- join the CTA's parts, in the line's order.  Parts of one unit are
+    // neighbours: lane k of every warp holds part k, a warp takes some heads.
+    const int4 part = lane < 2 * W ? slot[lane] : make_int4(-1, 0, 0, 0);
+    const uint32_t valid = __ballot_sync(0xffffffffu, part.x >= 0);
+    const uint32_t below = valid & ((1u << lane) - 1u);
+    const int prev = below ? 31 - __clz(below) : lane;
+    const int prev_b = __shfl_sync(0xffffffffu, part.x, prev), prev_hu = __shfl_sync(0xffffffffu, part.y, prev);
+    const uint32_t firsts =
+        __ballot_sync(0xffffffffu, part.x >= 0 && !(below && prev_b == part.x && prev_hu == part.y));
+    const uint32_t upto_here = firsts & (0xffffffffu >> (31 - lane)), after_here = firsts & ~(0xffffffffu >> (31 - lane));
+    const int first = upto_here ? 31 - __clz(upto_here) : 0;       // this lane's group of parts
+    const int end = after_here ? __ffs(after_here) - 2 : 31;
+    for (int h = warp; h < kHeads; h += W) {
+      const float2 st = part.x >= 0 ? slot_stat[lane][h] : make_float2(-INFINITY, 0.f);
+      float M = st.x;
+      for (int d = 1; d < 32; d <<= 1) {
+        const float v = __shfl_up_sync(0xffffffffu, M, d);
+        if (lane - d >= first) M = fmaxf(M, v);
       }
-      int end = i, j = i + 1;
-      for (; j < 2 * W; ++j) {
-        if (sl[j].x < 0) continue;
-        if (sl[j].x != u.x || sl[j].y != u.y) break;
-        end = j;
+      M = __shfl_sync(0xffffffffu, M, end);
+      const float w = weight(st.x, M);
+      float L = st.y * w;
+      for (int d = 1; d < 32; d <<= 1) {
+        const float v = __shfl_up_sync(0xffffffffu, L, d);
+        if (lane - d >= first) L += v;
       }
-      const bool ends = sl[end].w, whole = u.z && ends;
-      const int which = u.z ? 1 : 0;
-      const int kh = u.y / HT, h0 = u.y % HT * kHeads;
-      for (int x = threadIdx.x; x < kHeads * DP / 4; x += 32 * W) {
-        const int h = x / (DP / 4), d = x % (DP / 4) * 4;
-        float M = -INFINITY, L = 0.f;
-        for (int k = i; k <= end; ++k)
-          if (sl[k].x >= 0) M = fmaxf(M, slot_stat[k >> 1][k & 1][h].x);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = i; k <= end; ++k) {
-          if (sl[k].x < 0) continue;
-          const float2 st = slot_stat[k >> 1][k & 1][h];
-          const float w = weight(st.x, M);
-          const float* src = (k & 1) ? reinterpret_cast<const float*>(ring + (k >> 1) * S * Sh::kStage)
-                                     : ws.warp_o + (static_cast<size_t>(blockIdx.x) * W + (k >> 1)) * kHeads * DP;
-          const float4 p = *reinterpret_cast<const float4*>(src + h * DP + d);
-          L += st.y * w;
-          // a part without weight adds nothing, whatever it holds
-          if (st.x != -INFINITY || st.y != 0.f) {
-            v.x += p.x * w;
-            v.y += p.y * w;
-            v.z += p.z * w;
-            v.w += p.w * w;
-          }
-        }
-        if (whole) {
-          const float r = L == 0.f ? 0.f : 1.f / L;
-          if (h0 + h < G && d < D)
-            store_out4<X>(a, u.x, kh * G + h0 + h, d,
-                          L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                   : make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
-          if (d == 0 && a.lse && h0 + h < G)
-            a.lse[static_cast<int64_t>(u.x) * a.Hq + kh * G + h0 + h] = lse_of(M, L);
-        } else {
-          const size_t at = static_cast<size_t>(blockIdx.x) * 2 + which;
-          *reinterpret_cast<float4*>(ws.o + (at * kHeads + h) * DP + d) = v;
-          if (d == 0) ws.stat[at * kSlotHeads + h] = make_float2(M, L);
-        }
+      L = __shfl_sync(0xffffffffu, L, end);
+      if (part.x >= 0) {
+        // a part without weight is left out, whatever it holds (marked by -1)
+        slot_weight[lane][h] = st.x == -INFINITY && st.y == 0.f ? -1.f : w;
+        unit_stat[lane][h] = make_float2(M, L);
       }
-      if (u.z && !ends) {
-        // begins here, ends in a later CTA: the one that holds the unit's last tile
-        lead = make_int4(u.x, u.y, 0, 1);
-      }
-      i = j;
     }
-    if (lead.w && threadIdx.x == 0) {
-      // position of the unit's last tile on the line
-      int64_t at = 0;
-      for (int w = W - 1; w >= 0; --w) {
-        // the last warp with work knows the tiles before its first sequence
-        const int64_t wl = (static_cast<int64_t>(blockIdx.x) * W + w) * T / pieces;
-        const int64_t wh = (static_cast<int64_t>(blockIdx.x) * W + w + 1) * T / pieces;
-        if (wl < wh) {
-          at = start_before[w];
-          for (int b = start_b[w]; b < lead.x; ++b) at += (span_of(a, b).visible + 15) / 16;
-          break;
+    __syncthreads();
+    for (int x = threadIdx.x; x < kHeads * DP / 4; x += 32 * W) {
+      const int h = x / (DP / 4), d = x % (DP / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      int begins = 0;
+#pragma unroll 4
+      for (int k = 0; k < 2 * W; ++k) {
+        if (!(valid >> k & 1)) continue;
+        const float* src = (k & 1) ? reinterpret_cast<const float*>(ring + (k >> 1) * S * Sh::kStage)
+                                   : ws.warp_o + (static_cast<size_t>(blockIdx.x) * W + (k >> 1)) * kHeads * DP;
+        const float4 p = *reinterpret_cast<const float4*>(src + h * DP + d);
+        const float w = slot_weight[k][h];
+        if (firsts >> k & 1) {
+          v = make_float4(0.f, 0.f, 0.f, 0.f);
+          begins = slot[k].z;
+        }
+        if (!(w < 0.f)) {
+          v.x += p.x * w;
+          v.y += p.y * w;
+          v.z += p.z * w;
+          v.w += p.w * w;
+        }
+        const uint32_t later = valid & ~(0xffffffffu >> (31 - k));
+        if (later && !(firsts & later & (0u - later))) continue;     // the group goes on
+        const int4 u = slot[k];
+        const float2 st = unit_stat[k][h];
+        if (begins && u.w) {
+          const int kh = u.y / HT, hg = u.y % HT * kHeads + h;
+          const float r = st.y == 0.f ? 0.f : 1.f / st.y;
+          if (hg < G && d < D)
+            store_out4<X>(a, u.x, kh * G + hg, d,
+                          st.y == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                      : make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
+          if (d == 0 && a.lse && hg < G) a.lse[static_cast<int64_t>(u.x) * a.Hq + kh * G + hg] = lse_of(st.x, st.y);
+        } else {
+          // its beginning (slot 1) or a later part (slot 0) of a unit that goes on in other CTAs
+          const size_t at = static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0);
+          *reinterpret_cast<float4*>(ws.o + (at * kHeads + h) * DP + d) = v;
+          if (d == 0) ws.stat[at * kSlotHeads + h] = st;
         }
       }
-      const int64_t tiles = (span_of(a, lead.x).visible + 15) / 16;
-      const int64_t x = at * HU + (static_cast<int64_t>(lead.y) + 1) * tiles - 1;
-      lead.z = static_cast<int>(((x + 1) * ctas - 1) / T);
+    }
+    if (threadIdx.x == 0 && valid) {
+      const int4 u = slot[31 - __clz(valid)];
+      if (slot[31 - __clz(firsts)].z && !u.w) {
+        // begins here, ends in a later CTA: the one that holds the unit's last
+        // tile.  The last warp with work knows the line before its sequence.
+        int w = W - 1;
+        while (cut.start(blockIdx.x * W + w) == cut.start(blockIdx.x * W + w + 1)) --w;
+        int64_t at = start_before[w];
+        for (int b = start_b[w]; b < u.x; ++b) at += length(b);
+        lead = make_int4(u.x, u.y, cut.owner(at * HU + (static_cast<int64_t>(u.y) + 1) * length(u.x) - 1), 1);
+      }
     }
   }
   if (threadIdx.x == 0) ws.leader[blockIdx.x] = lead;
@@ -735,29 +808,42 @@ __global__ void __launch_bounds__(128) paged_attn_join_kernel(const __grid_const
   __shared__ float4 acc[kSplit][kLanes];
   pdl_wait();
   const Scratch ws = scratch_at<kHeads, DP>(a.ws);
-  const int4 lead = ws.leader[blockIdx.x];
-  if (!lead.w) return;
+  // the statistics of all CTAs that may follow are asked for with the leader's
+  // word, which says how many do
   const int h = blockIdx.y, D = a.cache.dim, G = a.Hq / a.cache.heads;
+  auto at = [&](int i) -> size_t {
+    return i == 0 ? static_cast<size_t>(blockIdx.x) * 2 + 1 : static_cast<size_t>(blockIdx.x + i) * 2;
+  };
+  const int after = gridDim.x - blockIdx.x;
+  const int4 lead = ws.leader[blockIdx.x];
+  float2 st[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = threadIdx.x + 128 * j;
+    st[j] = i < after ? ws.stat[at(i) * kSlotHeads + h] : make_float2(-INFINITY, 0.f);
+  }
+  if (!lead.w) return;
   const int HT = (G + kHeads - 1) / kHeads;
   const int kh = lead.y / HT, hg = lead.y % HT * kHeads + h;
   if (hg >= G) return;
   const int parts = lead.z - blockIdx.x + 1;
-  auto at = [&](int i) -> size_t {
-    return i == 0 ? static_cast<size_t>(blockIdx.x) * 2 + 1 : static_cast<size_t>(blockIdx.x + i) * 2;
-  };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float M = -INFINITY, L = 0.f;
-  for (int i = threadIdx.x; i < parts; i += 128) M = fmaxf(M, ws.stat[at(i) * kSlotHeads + h].x);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (threadIdx.x + 128 * j < parts) M = fmaxf(M, st[j].x);
   for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   if (lane == 0) red[0][warp] = M;
   __syncthreads();
   M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  for (int i = threadIdx.x; i < parts; i += 128) {
-    const float2 st = ws.stat[at(i) * kSlotHeads + h];
-    const float x = weight(st.x, M);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = threadIdx.x + 128 * j;
+    if (i >= parts) continue;
+    const float x = weight(st[j].x, M);
     // a part without weight is left out (marked by a negative factor)
-    w[i] = st.x == -INFINITY && st.y == 0.f ? -1.f : x;
-    L += st.y * x;
+    w[i] = st[j].x == -INFINITY && st[j].y == 0.f ? -1.f : x;
+    L += st[j].y * x;
   }
   for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
   if (lane == 0) red[1][warp] = L;
@@ -824,14 +910,20 @@ int split_ctas() {
   return n;
 }
 
-template <typename X, int DP, int NT, int BITS, int W, int S>
+template <typename X, int DP, int NT, int BITS, int W, int S, int TK>
 cudaError_t run(const PagedAttnArgs& a, cudaStream_t stream) {
   constexpr int QP = sizeof(X) == 2 ? 1 : 3;
-  using Sh = Shape<DP, NT, QP, BITS, W, S>;
-  auto kernel = paged_attn_kernel<X, DP, NT, QP, BITS, W, S>;
+  using Sh = Shape<DP, NT, QP, BITS, W, S, TK>;
+  auto kernel = paged_attn_kernel<X, DP, NT, QP, BITS, W, S, TK>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    // the same split of an SM's memory for both kernels: changing it between
+    // them would wait for the SM to drain
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(paged_attn_join_kernel<X, DP, NT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    return r;
   });
   if (e != cudaSuccess) return e;
   unsigned int* err = device_error_word();
@@ -842,36 +934,36 @@ cudaError_t run(const PagedAttnArgs& a, cudaStream_t stream) {
   return launch_pdl(paged_attn_join_kernel<X, DP, NT>, dim3(ctas, 8 * NT), 128, 0, stream, a);
 }
 
-// Warps and stages: the rings of all warps take most of the SM's shared
-// memory, so that two tiles of every warp are on the way (at least 128 KB).
+// Warps, stages and tokens of a tile: the rings of all warps take most of the
+// SM's shared memory, so that two tiles of every warp are on the way (at least
+// 128 KB); short rows come 32 to a tile.
 template <typename X, int NT>
 cudaError_t run_dim(const PagedAttnArgs& a, cudaStream_t stream) {
   const int D = a.cache.dim;
+  // fp32 q in three parts at the largest head dim: 16 heads do not fit registers
+  constexpr int kNT = sizeof(X) == 4 ? 1 : NT;
   if (a.cache.bits == 16) {
-    if (D <= 64) return run<X, 64, NT, 16, 16, 3>(a, stream);
-    if (D <= 128) return run<X, 128, NT, 16, 8, 3>(a, stream);
-    return run<X, 256, NT, 16, 4, 3>(a, stream);
+    if (D <= 64) return run<X, 64, NT, 16, 8, 3, 32>(a, stream);
+    if (D <= 128) return run<X, 128, NT, 16, 8, 3, 16>(a, stream);
+    return run<X, 256, kNT, 16, 4, 3, 16>(a, stream);
   }
-  if (D <= 64) return run<X, 64, NT, 8, 16, 4>(a, stream);
-  if (D <= 128) return run<X, 128, NT, 8, 16, 3>(a, stream);
-  return run<X, 256, NT, 8, 8, 3>(a, stream);
+  if (D <= 64) return run<X, 64, NT, 8, 16, 3, 32>(a, stream);
+  if (D <= 128) return run<X, 128, NT, 8, 8, 3, 32>(a, stream);
+  return run<X, 256, kNT, 8, 8, 3, 16>(a, stream);
 }
-
-// 16 heads a unit when the group has more than 8, unless their registers do
-// not fit (fp32 q in three parts at the largest head dim).
-bool two_columns(int G, int D, bool f32) { return G > 8 && !(f32 && D > 128); }
 
 }  // namespace
 
 size_t paged_attn_ws_bytes(int Hq, int heads, int dim) {
   const size_t dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-  const size_t h = Hq / heads > 8 ? 16 : 8, warps = 16;
+  const size_t h = Hq / heads > 8 ? 16 : 8, warps = dim <= 64 ? 16 : 8;
   return scratch_head_bytes() + static_cast<size_t>(kMaxCtas) * (2 + warps) * h * dp * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   const bool f32 = a.qdt == QVLA_DTYPE_F32;
-  if (two_columns(a.Hq / a.cache.heads, a.cache.dim, f32))
+  // a unit is a key head with 8, or (for larger groups) 16 of its query heads
+  if (a.Hq / a.cache.heads > 8)
     return f32 ? run_dim<float, 2>(a, stream) : run_dim<__nv_bfloat16, 2>(a, stream);
   return f32 ? run_dim<float, 1>(a, stream) : run_dim<__nv_bfloat16, 1>(a, stream);
 }
