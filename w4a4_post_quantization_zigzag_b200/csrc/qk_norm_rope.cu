@@ -5,6 +5,8 @@
 #include "qvla_common.cuh"
 #include "qvla_internal.h"
 
+#include <algorithm>
+
 namespace qvla {
 namespace {
 
@@ -25,22 +27,9 @@ struct Vec8 {
   float v[8];
 };
 
-template <typename X>
-QVLA_DEVICE Vec8 load8(const X* p) {
-  Vec8 r;
-  if constexpr (sizeof(X) == 2) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.v[2 * i] = __uint_as_float(u[i] << 16);
-      r.v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    r = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-  }
-  return r;
+QVLA_DEVICE Vec8 load8(const float* p) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 
 QVLA_DEVICE uint32_t pack_bf16(float lo, float hi) {
@@ -76,18 +65,64 @@ QVLA_DEVICE void store_codes(int8_t* p, const Vec8& r, float s) {
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
-// One CTA per token.  A head's row of D values belongs to LPR = 4, 8 or 16
-// lanes of a warp; a lane holds two chunks of eight values that hold whole
-// rotation pairs (for separate halves: chunk j and chunk j + rot/16 of the
-// row), so norm, rotation and stores need no exchange but the sum of squares
-// (and the maximum, for 8-bit codes).  A lane writes only what it read, so
-// q_out and k_out may be the inputs.
+// Raw chunk of eight values as it is loaded (a pass ahead of its use).
+template <typename X>
+struct Raw8 {
+  uint4 v[sizeof(X) == 2 ? 1 : 2];
+};
+template <typename X>
+QVLA_DEVICE Raw8<X> load_raw(const X* p) {
+  Raw8<X> r;
+  r.v[0] = reinterpret_cast<const uint4*>(p)[0];
+  if constexpr (sizeof(X) == 4) r.v[1] = reinterpret_cast<const uint4*>(p)[1];
+  return r;
+}
+template <typename X>
+QVLA_DEVICE Vec8 widen(const Raw8<X>& w) {
+  Vec8 r;
+  const uint32_t u[4] = {w.v[0].x, w.v[0].y, w.v[0].z, w.v[0].w};
+  if constexpr (sizeof(X) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.v[2 * i] = __uint_as_float(u[i] << 16);
+      r.v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  } else {
+    const uint4 h = w.v[sizeof(X) == 2 ? 0 : 1];
+    const uint32_t q[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.v[i] = __uint_as_float(u[i]);
+      r.v[4 + i] = __uint_as_float(q[i]);
+    }
+  }
+  return r;
+}
+
+// A token's rows (query, key, value heads) are dealt to `share` warps, which
+// go on to further tokens.
+struct RowShare {
+  int share;           // warps of a token
+  int passes;          // passes of 32 / LPR rows that one of them takes
+  int64_t items;       // T * share
+};
+
+// Bound by reading the rows and writing them back.  A head's row of D values
+// belongs to LPR = 4, 8 or 16 lanes of a warp; a lane holds two chunks of eight
+// values that hold whole rotation pairs (for separate halves: chunk j and chunk
+// j + rot/16 of the row), so norm, rotation and stores need no exchange but the
+// sum of squares (and the maximum, for 8-bit codes).  A lane writes only what it
+// read, so q_out and k_out may be the inputs.  The next pass's rows are loaded
+// before this pass's are worked on: with 24 warps on an SM that keeps 48 KB on
+// the way.
 template <typename X, int LPR>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormRopeArgs a,
-                                                        unsigned int* err) {
-  const int t = blockIdx.x;
-  const int sub = threadIdx.x % LPR, items = a.D / 16;
-  const bool on = sub < items;
+__global__ void __launch_bounds__(256, sizeof(X) == 2 ? 3 : 2)
+    norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ RowShare sh,
+                     unsigned int* err) {
+  constexpr int kRows = 32 / LPR;          // rows of a pass
+  const int lane = threadIdx.x & 31;
+  const int sub = lane % LPR;
+  const bool on = sub < a.D / 16;
   const int pairs = a.rot / 16;            // lanes whose chunks are rotated
   const bool turn = sub < pairs;
   // the two chunks of this lane (in units of eight values)
@@ -96,109 +131,136 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
     c0 = sub;
     c1 = sub + pairs;
   }
-  bool bad = false;
-  Vec8 cs, sn;
-  if (a.table) {
-    const int p = a.positions[t];
-    bad = p < 0 || p >= a.P;
-    if (!bad && on && turn) {
-      const float* row = a.table + static_cast<int64_t>(p) * a.rot + sub * 8;
+  const int heads = a.Hq + a.Hkv + (a.has_cache ? a.Hkv : 0);
+  const float inv_dim = 1.f / static_cast<float>(a.D);
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // row h of token t: query, key or value head; its place in the inputs
+  struct Place {
+    int kind, head;          // 0 query, 1 key, 2 value, 3 none
+    const X* x;
+  };
+  auto place = [&](int t, int h) -> Place {
+    Place p;
+    p.kind = !on || h >= heads ? 3 : h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
+    p.head = h - (p.kind == 0 ? 0 : p.kind == 1 ? a.Hq : a.Hq + a.Hkv);
+    const void* base = p.kind == 0 ? a.q : p.kind == 1 ? a.k : a.v;
+    const int64_t ld = p.kind == 0 ? a.ldq : p.kind == 1 ? a.ldk : a.ldv;
+    p.x = static_cast<const X*>(base) + t * ld + static_cast<int64_t>(p.head) * a.D;
+    return p;
+  };
+
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); item < sh.items; item += step) {
+    const int t = static_cast<int>(item / sh.share), part = static_cast<int>(item - static_cast<int64_t>(t) * sh.share);
+    const int h0 = part * sh.passes * kRows + lane / LPR;
+    const int pos = a.table ? a.positions[t] : 0;
+    const int s = a.has_cache ? a.slots[t] : -1;
+    Place now = place(t, h0);
+    Raw8<X> r0 = {}, r1 = {};
+    if (now.kind < 3) {
+      r0 = load_raw(now.x + c0 * 8);
+      r1 = load_raw(now.x + c1 * 8);
+    }
+    const bool bad = a.table && (pos < 0 || pos >= a.P);
+    Vec8 cs = {}, sn = {};
+    if (a.table && !bad && on && turn) {
+      const float* row = a.table + static_cast<int64_t>(pos) * a.rot + sub * 8;
       cs = load8(row);
       sn = load8(row + a.rot / 2);
     }
-  }
-  int64_t slot_off = -1, scale_off = 0;
-  if (a.has_cache) {
-    const int s = a.slots[t];
-    const int page = s / a.cache.page_size, tok = s - page * a.cache.page_size;
-    if (s >= 0 && page >= a.cache.pages) {
-      if (threadIdx.x == 0) report(err, QVLA_DEVERR_CACHE_RANGE);
-    } else if (s >= 0 && !bad) {
-      slot_off = page * a.cache.page_stride + tok * a.cache.token_stride;
-      scale_off = page * a.cache.s_page_stride + tok * a.cache.s_token_stride;
+    int64_t slot_off = -1, scale_off = 0;
+    if (s >= 0) {
+      const int page = s / a.cache.page_size, tok = s - page * a.cache.page_size;
+      if (page < a.cache.pages && !bad) {
+        slot_off = page * a.cache.page_stride + tok * a.cache.token_stride;
+        scale_off = page * a.cache.s_page_stride + tok * a.cache.s_token_stride;
+      }
+      if (page >= a.cache.pages && part == 0 && lane == 0) report(err, QVLA_DEVERR_CACHE_RANGE);
     }
-  }
-  if (bad && threadIdx.x == 0) report(err, QVLA_DEVERR_CACHE_RANGE);
+    if (bad && part == 0 && lane == 0) report(err, QVLA_DEVERR_CACHE_RANGE);
 
-  const int heads = a.Hq + a.Hkv + (a.has_cache ? a.Hkv : 0);
-  for (int h0 = 0; h0 < heads; h0 += blockDim.x / LPR) {   // whole warps stay together
-    const int h = h0 + static_cast<int>(threadIdx.x) / LPR;
-    const bool live = on && h < heads;
-    const int kind = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;    // query, key, value
-    const int hh = kind == 0 ? h : kind == 1 ? h - a.Hq : h - a.Hq - a.Hkv;
-    Vec8 x0 = {}, x1 = {};
-    if (live) {
-      const void* base = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-      const int64_t ld = kind == 0 ? a.ldq : kind == 1 ? a.ldk : a.ldv;
-      const X* row = static_cast<const X*>(base) + t * ld + static_cast<int64_t>(hh) * a.D;
-      x0 = load8(row + c0 * 8);
-      x1 = load8(row + c1 * 8);
-    }
-    const float* w = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x0.v[i] * x0.v[i] + x1.v[i] * x1.v[i];
-#pragma unroll
-    for (int d = LPR / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    if (live && w) {
-      const float r = 1.f / sqrtf(ss / static_cast<float>(a.D) + a.eps);
-      const Vec8 w0 = load8(w + c0 * 8), w1 = load8(w + c1 * 8);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x0.v[i] = x0.v[i] * r * w0.v[i];
-        x1.v[i] = x1.v[i] * r * w1.v[i];
-      }
-    }
-    if (live && turn && kind < 2 && !bad) {
-      if (a.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p0 = x0.v[2 * i], q0 = x0.v[2 * i + 1], p1 = x1.v[2 * i], q1 = x1.v[2 * i + 1];
-          x0.v[2 * i] = p0 * cs.v[i] - q0 * sn.v[i];
-          x0.v[2 * i + 1] = q0 * cs.v[i] + p0 * sn.v[i];
-          x1.v[2 * i] = p1 * cs.v[4 + i] - q1 * sn.v[4 + i];
-          x1.v[2 * i + 1] = q1 * cs.v[4 + i] + p1 * sn.v[4 + i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = x0.v[i], q = x1.v[i];
-          x0.v[i] = p * cs.v[i] - q * sn.v[i];
-          x1.v[i] = q * cs.v[i] + p * sn.v[i];
+#pragma unroll 1
+    for (int i = 0; i < sh.passes; ++i) {
+      Vec8 x0 = widen<X>(r0), x1 = widen<X>(r1);
+      const Place at = now;
+      if (i + 1 < sh.passes) {
+        now = place(t, h0 + (i + 1) * kRows);
+        if (now.kind < 3) {
+          r0 = load_raw(now.x + c0 * 8);
+          r1 = load_raw(now.x + c1 * 8);
+        } else {
+          r0 = r1 = Raw8<X>{};
         }
       }
-    }
-    if (bad) x0 = x1 = Vec8{};
-    if (live && kind < 2) {
-      void* base = kind == 0 ? a.q_out : a.k_out;
-      if (base) {
-        X* row = static_cast<X*>(base) + t * (kind == 0 ? a.ldqo : a.ldko) + static_cast<int64_t>(hh) * a.D;
+      const float* w = at.kind == 0 ? a.q_norm : at.kind == 1 ? a.k_norm : nullptr;
+      if (a.q_norm || a.k_norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x0.v[j], x0.v[j], fmaf(x1.v[j], x1.v[j], ss));
+#pragma unroll
+        for (int d = LPR / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        if (at.kind < 2 && w) {
+          const float r = 1.f / sqrtf(fmaf(ss, inv_dim, a.eps));
+          const Vec8 w0 = load8(w + c0 * 8), w1 = load8(w + c1 * 8);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x0.v[j] = x0.v[j] * r * w0.v[j];
+            x1.v[j] = x1.v[j] * r * w1.v[j];
+          }
+        }
+      }
+      if (at.kind < 2 && turn && !bad) {
+        if (a.interleaved) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p0 = x0.v[2 * j], q0 = x0.v[2 * j + 1], p1 = x1.v[2 * j], q1 = x1.v[2 * j + 1];
+            x0.v[2 * j] = p0 * cs.v[j] - q0 * sn.v[j];
+            x0.v[2 * j + 1] = q0 * cs.v[j] + p0 * sn.v[j];
+            x1.v[2 * j] = p1 * cs.v[4 + j] - q1 * sn.v[4 + j];
+            x1.v[2 * j + 1] = q1 * cs.v[4 + j] + p1 * sn.v[4 + j];
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float p = x0.v[j], q = x1.v[j];
+            x0.v[j] = p * cs.v[j] - q * sn.v[j];
+            x1.v[j] = q * cs.v[j] + p * sn.v[j];
+          }
+        }
+      }
+      if (bad) x0 = x1 = Vec8{};
+      if (at.kind < 2) {
+        void* base = at.kind == 0 ? a.q_out : a.k_out;
+        if (base) {
+          X* row = static_cast<X*>(base) + t * (at.kind == 0 ? a.ldqo : a.ldko) + static_cast<int64_t>(at.head) * a.D;
+          store8(row + c0 * 8, x0);
+          store8(row + c1 * 8, x1);
+        }
+      }
+      if (!a.has_cache) continue;
+      const bool store = (at.kind == 1 || at.kind == 2) && slot_off >= 0;
+      const int64_t to = slot_off + at.head * a.cache.head_stride;
+      if (a.cache.bits == 8) {
+        float mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(fabsf(x0.v[j]), fabsf(x1.v[j])));
+#pragma unroll
+        for (int d = LPR / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        if (store) {
+          const float q = __fdiv_rn(mx, 127.f);
+          int8_t* row = static_cast<int8_t*>(at.kind == 1 ? a.cache.k : a.cache.v) + to;
+          store_codes(row + c0 * 8, x0, q);
+          store_codes(row + c1 * 8, x1, q);
+          if (sub == 0)
+            (at.kind == 1 ? a.cache.k_scale : a.cache.v_scale)[scale_off + at.head * a.cache.s_head_stride] = q;
+        }
+      } else if (store) {
+        __nv_bfloat16* row = static_cast<__nv_bfloat16*>(at.kind == 1 ? a.cache.k : a.cache.v) + to;
         store8(row + c0 * 8, x0);
         store8(row + c1 * 8, x1);
       }
-    }
-    if (kind == 0 || slot_off < 0) {
-      if (a.cache.bits != 8) continue;
-    }
-    const int64_t at = slot_off + hh * a.cache.head_stride;
-    if (a.cache.bits == 8) {
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fmaxf(fabsf(x0.v[i]), fabsf(x1.v[i])));
-#pragma unroll
-      for (int d = LPR / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      if (live && kind > 0 && slot_off >= 0) {
-        const float s = __fdiv_rn(mx, 127.f);
-        int8_t* row = static_cast<int8_t*>(kind == 1 ? a.cache.k : a.cache.v) + at;
-        store_codes(row + c0 * 8, x0, s);
-        store_codes(row + c1 * 8, x1, s);
-        if (sub == 0)
-          (kind == 1 ? a.cache.k_scale : a.cache.v_scale)[scale_off + hh * a.cache.s_head_stride] = s;
-      }
-    } else if (live) {
-      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(kind == 1 ? a.cache.k : a.cache.v) + at;
-      store8(row + c0 * 8, x0);
-      store8(row + c1 * 8, x1);
     }
   }
 }
@@ -207,10 +269,29 @@ template <typename X, int LPR>
 cudaError_t launch_typed(const NormRopeArgs& a, cudaStream_t stream) {
   unsigned int* err = device_error_word();
   if (!err) return cudaErrorUnknown;
-  const int64_t heads = static_cast<int64_t>(a.Hq) + a.Hkv + (a.has_cache ? a.Hkv : 0);
-  const int64_t lanes = (heads * LPR + 31) / 32 * 32;
-  norm_rope_kernel<X, LPR><<<a.T, static_cast<int>(lanes < 256 ? lanes : 256), 0, stream>>>(a, err);
-  return cudaGetLastError();
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int resident = sms * (sizeof(X) == 2 ? 3 : 2);             // CTAs at once
+  const int heads = a.Hq + a.Hkv + (a.has_cache ? a.Hkv : 0);
+  const int passes = (heads + 32 / LPR - 1) / (32 / LPR);
+  // with fewer tokens than warps, several warps share a token
+  RowShare sh;
+  const int want = static_cast<int>(std::min<int64_t>(passes, std::max<int64_t>(1, 8ll * resident / a.T)));
+  sh.passes = (passes + want - 1) / want;
+  sh.share = (passes + sh.passes - 1) / sh.passes;
+  sh.items = static_cast<int64_t>(a.T) * sh.share;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((sh.items + 7) / 8, resident)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<X, LPR>, a, sh, err);
 }
 
 }  // namespace
