@@ -99,13 +99,159 @@ QVLA_DEVICE Vec8 widen(const Raw8<X>& w) {
   return r;
 }
 
-// A token's rows (query, key, value heads) are dealt to `share` warps, which
-// go on to further tokens.
+// A token's heads go by in passes of 32 / LPR rows: query passes, key passes,
+// value passes.  `share` warps take `each` passes of a token, and go on to
+// further tokens.
 struct RowShare {
-  int share;           // warps of a token
-  int passes;          // passes of 32 / LPR rows that one of them takes
-  int64_t items;       // T * share
+  int query, key, all;     // passes before the key's, before the value's, of a token
+  int share, each;
+  int64_t items;           // T * share
 };
+
+// Where a lane's values lie in a row, and what its token says.
+template <typename X>
+struct Lane {
+  int c0, c1;              // its two chunks
+  int row;                 // its row of a pass
+  bool on, turn;           // it has values, they are rotated
+  int pos;
+  bool bad;                // position outside the table
+  int64_t slot_off, scale_off;   // of the token's slot; slot_off < 0: nothing is written
+};
+
+// Passes [lo, hi) of one kind of head (0 query, 1 key, 2 value) of a token.
+// With norm weight w and r = 1 / sqrt(mean + eps), pairs become
+//   (a, b) -> r (a (w_a c) - b (w_b s)),  r (b (w_b c) + a (w_a s)):
+// four coefficients a pair, formed once here.
+template <typename X, int LPR, bool INTER, int KIND>
+QVLA_DEVICE void some_heads(const NormRopeArgs& a, const Lane<X>& ln, int t, int lo, int hi) {
+  if (lo >= hi) return;
+  constexpr int kRows = 32 / LPR;
+  const int H = KIND == 0 ? a.Hq : a.Hkv;
+  int h = lo * kRows + ln.row;
+  const X* x = (KIND == 0   ? static_cast<const X*>(a.q) + t * a.ldq
+                : KIND == 1 ? static_cast<const X*>(a.k) + t * a.ldk
+                            : static_cast<const X*>(a.v) + t * a.ldv) +
+               h * a.D;
+  X* out = KIND == 0   ? static_cast<X*>(a.q_out) + t * a.ldqo + h * a.D
+           : KIND == 1 ? static_cast<X*>(a.k_out) + t * a.ldko + h * a.D
+                       : nullptr;
+  const bool to_out = KIND == 0 || (KIND == 1 && a.k_out != nullptr);
+  const bool to_cache = KIND > 0 && a.has_cache && ln.slot_off >= 0;
+  int64_t at = ln.slot_off + h * a.cache.head_stride, scale_at = ln.scale_off + h * a.cache.s_head_stride;
+  const float* w = KIND == 0 ? a.q_norm : KIND == 1 ? a.k_norm : nullptr;
+  Raw8<X> r0 = {}, r1 = {};
+  if (ln.on && h < H) {
+    r0 = load_raw(x + ln.c0);
+    r1 = load_raw(x + ln.c1);
+  }
+  Vec8 p0, p1, q0, q1;
+  if constexpr (KIND < 2) {
+    if (w && ln.on) {
+      p0 = load8(w + ln.c0);
+      p1 = load8(w + ln.c1);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p0.v[j] = p1.v[j] = 1.f;
+    }
+    if (ln.turn && !ln.bad) {
+      const float* row = a.table + static_cast<int64_t>(ln.pos) * a.rot + (threadIdx.x % LPR) * 8;
+      const Vec8 cs = load8(row), sn = load8(row + a.rot / 2);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (INTER) {
+          q0.v[j] = p0.v[j ^ 1] * (j & 1 ? sn.v[j / 2] : -sn.v[j / 2]);
+          q1.v[j] = p1.v[j ^ 1] * (j & 1 ? sn.v[4 + j / 2] : -sn.v[4 + j / 2]);
+        } else {
+          q0.v[j] = -p1.v[j] * sn.v[j];
+          q1.v[j] = p0.v[j] * sn.v[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p0.v[j] *= cs.v[INTER ? j / 2 : j];
+        p1.v[j] *= cs.v[INTER ? 4 + j / 2 : j];
+      }
+    }
+  }
+#pragma unroll 1
+  for (int i = lo; i < hi; ++i) {
+    const bool live = ln.on && h < H;
+    Vec8 x0 = widen<X>(r0), x1 = widen<X>(r1);
+    h += kRows;
+    x += kRows * a.D;
+    if (i + 1 < hi && ln.on && h < H) {
+      r0 = load_raw(x + ln.c0);
+      r1 = load_raw(x + ln.c1);
+    } else {
+      r0 = r1 = Raw8<X>{};
+    }
+    if constexpr (KIND < 2) {
+      float r = 1.f;
+      if (w) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x0.v[j], x0.v[j], fmaf(x1.v[j], x1.v[j], ss));
+#pragma unroll
+        for (int d = LPR / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        r = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
+      }
+      if (ln.bad) {
+        x0 = x1 = Vec8{};
+      } else if (ln.turn) {
+        const Vec8 y0 = x0, y1 = x1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x0.v[j] = fmaf(y0.v[j], p0.v[j], (INTER ? y0.v[j ^ 1] : y1.v[j]) * q0.v[j]) * r;
+          x1.v[j] = fmaf(y1.v[j], p1.v[j], (INTER ? y1.v[j ^ 1] : y0.v[j]) * q1.v[j]) * r;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x0.v[j] = x0.v[j] * p0.v[j] * r;
+          x1.v[j] = x1.v[j] * p1.v[j] * r;
+        }
+      }
+      if (to_out) {
+        if (live) {
+          store8(out + ln.c0, x0);
+          store8(out + ln.c1, x1);
+        }
+        out += kRows * a.D;
+      }
+    }
+    if constexpr (KIND > 0) {
+      if (!to_cache) continue;               // the same for the whole warp
+      if (a.cache.bits == 8) {
+        float mx = 0.f;
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(fabsf(x0.v[j]), fabsf(x1.v[j])));
+        }
+#pragma unroll
+        for (int d = LPR / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        if (live) {
+          const float s = __fdiv_rn(mx, 127.f);
+          int8_t* row = static_cast<int8_t*>(KIND == 1 ? a.cache.k : a.cache.v) + at;
+          store_codes(row + ln.c0, x0, s);
+          store_codes(row + ln.c1, x1, s);
+          if (threadIdx.x % LPR == 0) (KIND == 1 ? a.cache.k_scale : a.cache.v_scale)[scale_at] = s;
+        }
+        scale_at += kRows * a.cache.s_head_stride;
+      } else if (live) {
+        __nv_bfloat16* row = static_cast<__nv_bfloat16*>(KIND == 1 ? a.cache.k : a.cache.v) + at;
+        store8(row + ln.c0, x0);
+        store8(row + ln.c1, x1);
+      }
+      at += kRows * a.cache.head_stride;
+    }
+  }
+}
+
+// CTAs of 256 threads per SM: with three, at 80 registers, the coefficients spill
+// (16381 x 48 heads of 128: 94 against 85 us); rows two or more passes ahead
+// change nothing there (85 to 88 us).
+constexpr int kResident = 2;
 
 // Bound by reading the rows and writing them back.  A head's row of D values
 // belongs to LPR = 4, 8 or 16 lanes of a warp; a lane holds two chunks of eight
@@ -113,155 +259,47 @@ struct RowShare {
 // j + rot/16 of the row), so norm, rotation and stores need no exchange but the
 // sum of squares (and the maximum, for 8-bit codes).  A lane writes only what it
 // read, so q_out and k_out may be the inputs.  The next pass's rows are loaded
-// before this pass's are worked on: with 24 warps on an SM that keeps 48 KB on
-// the way.
-template <typename X, int LPR>
-__global__ void __launch_bounds__(256, sizeof(X) == 2 ? 3 : 2)
+// before this pass's are worked on.
+template <typename X, int LPR, bool INTER>
+__global__ void __launch_bounds__(256, kResident)
     norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ RowShare sh,
                      unsigned int* err) {
-  constexpr int kRows = 32 / LPR;          // rows of a pass
-  const int lane = threadIdx.x & 31;
-  const int sub = lane % LPR;
-  const bool on = sub < a.D / 16;
-  const int pairs = a.rot / 16;            // lanes whose chunks are rotated
-  const bool turn = sub < pairs;
-  // the two chunks of this lane (in units of eight values)
-  int c0 = 2 * sub, c1 = 2 * sub + 1;
-  if (turn && !a.interleaved) {
-    c0 = sub;
-    c1 = sub + pairs;
+  const int lane = threadIdx.x & 31, sub = lane % LPR;
+  Lane<X> ln;
+  ln.on = sub < a.D / 16;
+  ln.turn = sub < a.rot / 16;
+  ln.row = lane / LPR;
+  ln.c0 = 16 * sub;
+  ln.c1 = 16 * sub + 8;
+  if (ln.turn && !INTER) {
+    ln.c0 = 8 * sub;
+    ln.c1 = 8 * sub + a.rot / 2;
   }
-  const int heads = a.Hq + a.Hkv + (a.has_cache ? a.Hkv : 0);
-  const float inv_dim = 1.f / static_cast<float>(a.D);
   pdl_launch_dependents();
   pdl_wait();
-
-  // row h of token t: query, key or value head; its place in the inputs
-  struct Place {
-    int kind, head;          // 0 query, 1 key, 2 value, 3 none
-    const X* x;
-  };
-  auto place = [&](int t, int h) -> Place {
-    Place p;
-    p.kind = !on || h >= heads ? 3 : h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
-    p.head = h - (p.kind == 0 ? 0 : p.kind == 1 ? a.Hq : a.Hq + a.Hkv);
-    const void* base = p.kind == 0 ? a.q : p.kind == 1 ? a.k : a.v;
-    const int64_t ld = p.kind == 0 ? a.ldq : p.kind == 1 ? a.ldk : a.ldv;
-    p.x = static_cast<const X*>(base) + t * ld + static_cast<int64_t>(p.head) * a.D;
-    return p;
-  };
-
   const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); item < sh.items; item += step) {
-    const int t = static_cast<int>(item / sh.share), part = static_cast<int>(item - static_cast<int64_t>(t) * sh.share);
-    const int h0 = part * sh.passes * kRows + lane / LPR;
-    const int pos = a.table ? a.positions[t] : 0;
+    const int t = sh.share == 1 ? static_cast<int>(item) : static_cast<int>(item / sh.share);
+    const int lo = static_cast<int>(item - static_cast<int64_t>(t) * sh.share) * sh.each;
+    const int hi = min(lo + sh.each, sh.all);
+    ln.pos = a.table ? a.positions[t] : 0;
     const int s = a.has_cache ? a.slots[t] : -1;
-    Place now = place(t, h0);
-    Raw8<X> r0 = {}, r1 = {};
-    if (now.kind < 3) {
-      r0 = load_raw(now.x + c0 * 8);
-      r1 = load_raw(now.x + c1 * 8);
-    }
-    const bool bad = a.table && (pos < 0 || pos >= a.P);
-    Vec8 cs = {}, sn = {};
-    if (a.table && !bad && on && turn) {
-      const float* row = a.table + static_cast<int64_t>(pos) * a.rot + sub * 8;
-      cs = load8(row);
-      sn = load8(row + a.rot / 2);
-    }
-    int64_t slot_off = -1, scale_off = 0;
+    ln.bad = a.table && (ln.pos < 0 || ln.pos >= a.P);
+    ln.slot_off = -1;
+    ln.scale_off = 0;
+    bool outside = ln.bad;
     if (s >= 0) {
       const int page = s / a.cache.page_size, tok = s - page * a.cache.page_size;
-      if (page < a.cache.pages && !bad) {
-        slot_off = page * a.cache.page_stride + tok * a.cache.token_stride;
-        scale_off = page * a.cache.s_page_stride + tok * a.cache.s_token_stride;
-      }
-      if (page >= a.cache.pages && part == 0 && lane == 0) report(err, QVLA_DEVERR_CACHE_RANGE);
-    }
-    if (bad && part == 0 && lane == 0) report(err, QVLA_DEVERR_CACHE_RANGE);
-
-#pragma unroll 1
-    for (int i = 0; i < sh.passes; ++i) {
-      Vec8 x0 = widen<X>(r0), x1 = widen<X>(r1);
-      const Place at = now;
-      if (i + 1 < sh.passes) {
-        now = place(t, h0 + (i + 1) * kRows);
-        if (now.kind < 3) {
-          r0 = load_raw(now.x + c0 * 8);
-          r1 = load_raw(now.x + c1 * 8);
-        } else {
-          r0 = r1 = Raw8<X>{};
-        }
-      }
-      const float* w = at.kind == 0 ? a.q_norm : at.kind == 1 ? a.k_norm : nullptr;
-      if (a.q_norm || a.k_norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x0.v[j], x0.v[j], fmaf(x1.v[j], x1.v[j], ss));
-#pragma unroll
-        for (int d = LPR / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        if (at.kind < 2 && w) {
-          const float r = 1.f / sqrtf(fmaf(ss, inv_dim, a.eps));
-          const Vec8 w0 = load8(w + c0 * 8), w1 = load8(w + c1 * 8);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x0.v[j] = x0.v[j] * r * w0.v[j];
-            x1.v[j] = x1.v[j] * r * w1.v[j];
-          }
-        }
-      }
-      if (at.kind < 2 && turn && !bad) {
-        if (a.interleaved) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float p0 = x0.v[2 * j], q0 = x0.v[2 * j + 1], p1 = x1.v[2 * j], q1 = x1.v[2 * j + 1];
-            x0.v[2 * j] = p0 * cs.v[j] - q0 * sn.v[j];
-            x0.v[2 * j + 1] = q0 * cs.v[j] + p0 * sn.v[j];
-            x1.v[2 * j] = p1 * cs.v[4 + j] - q1 * sn.v[4 + j];
-            x1.v[2 * j + 1] = q1 * cs.v[4 + j] + p1 * sn.v[4 + j];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float p = x0.v[j], q = x1.v[j];
-            x0.v[j] = p * cs.v[j] - q * sn.v[j];
-            x1.v[j] = q * cs.v[j] + p * sn.v[j];
-          }
-        }
-      }
-      if (bad) x0 = x1 = Vec8{};
-      if (at.kind < 2) {
-        void* base = at.kind == 0 ? a.q_out : a.k_out;
-        if (base) {
-          X* row = static_cast<X*>(base) + t * (at.kind == 0 ? a.ldqo : a.ldko) + static_cast<int64_t>(at.head) * a.D;
-          store8(row + c0 * 8, x0);
-          store8(row + c1 * 8, x1);
-        }
-      }
-      if (!a.has_cache) continue;
-      const bool store = (at.kind == 1 || at.kind == 2) && slot_off >= 0;
-      const int64_t to = slot_off + at.head * a.cache.head_stride;
-      if (a.cache.bits == 8) {
-        float mx = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(fabsf(x0.v[j]), fabsf(x1.v[j])));
-#pragma unroll
-        for (int d = LPR / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        if (store) {
-          const float q = __fdiv_rn(mx, 127.f);
-          int8_t* row = static_cast<int8_t*>(at.kind == 1 ? a.cache.k : a.cache.v) + to;
-          store_codes(row + c0 * 8, x0, q);
-          store_codes(row + c1 * 8, x1, q);
-          if (sub == 0)
-            (at.kind == 1 ? a.cache.k_scale : a.cache.v_scale)[scale_off + at.head * a.cache.s_head_stride] = q;
-        }
-      } else if (store) {
-        __nv_bfloat16* row = static_cast<__nv_bfloat16*>(at.kind == 1 ? a.cache.k : a.cache.v) + to;
-        store8(row + c0 * 8, x0);
-        store8(row + c1 * 8, x1);
+      outside |= page >= a.cache.pages;
+      if (!outside) {
+        ln.slot_off = page * a.cache.page_stride + tok * a.cache.token_stride;
+        ln.scale_off = page * a.cache.s_page_stride + tok * a.cache.s_token_stride;
       }
     }
+    if (outside && lo == 0 && lane == 0) report(err, QVLA_DEVERR_CACHE_RANGE);
+    some_heads<X, LPR, INTER, 0>(a, ln, t, lo, min(hi, sh.query));
+    some_heads<X, LPR, INTER, 1>(a, ln, t, max(lo - sh.query, 0), min(hi, sh.key) - sh.query);
+    some_heads<X, LPR, INTER, 2>(a, ln, t, max(lo - sh.key, 0), hi - sh.key);
   }
 }
 
@@ -273,14 +311,16 @@ cudaError_t launch_typed(const NormRopeArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int resident = sms * (sizeof(X) == 2 ? 3 : 2);             // CTAs at once
-  const int heads = a.Hq + a.Hkv + (a.has_cache ? a.Hkv : 0);
-  const int passes = (heads + 32 / LPR - 1) / (32 / LPR);
-  // with fewer tokens than warps, several warps share a token
+  const int64_t resident = sms * kResident;
+  constexpr int kRows = 32 / LPR;
   RowShare sh;
-  const int want = static_cast<int>(std::min<int64_t>(passes, std::max<int64_t>(1, 8ll * resident / a.T)));
-  sh.passes = (passes + want - 1) / want;
-  sh.share = (passes + sh.passes - 1) / sh.passes;
+  sh.query = (a.Hq + kRows - 1) / kRows;
+  sh.key = sh.query + (a.Hkv + kRows - 1) / kRows;
+  sh.all = sh.key + (a.has_cache ? (a.Hkv + kRows - 1) / kRows : 0);
+  // with fewer tokens than warps, several warps share a token
+  const int want = static_cast<int>(std::min<int64_t>(sh.all, std::max<int64_t>(1, 8 * resident / a.T)));
+  sh.each = (sh.all + want - 1) / want;
+  sh.share = (sh.all + sh.each - 1) / sh.each;
   sh.items = static_cast<int64_t>(a.T) * sh.share;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((sh.items + 7) / 8, resident)));
@@ -291,7 +331,8 @@ cudaError_t launch_typed(const NormRopeArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<X, LPR>, a, sh, err);
+  if (a.interleaved) return cudaLaunchKernelEx(&cfg, norm_rope_kernel<X, LPR, true>, a, sh, err);
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<X, LPR, false>, a, sh, err);
 }
 
 }  // namespace
