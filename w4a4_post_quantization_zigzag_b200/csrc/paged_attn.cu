@@ -454,12 +454,13 @@ __global__ void __launch_bounds__(32 * W, 1)
 
       const uint32_t kt = ring0 + stage * Sh::kStage, vt = kt + Sh::kTile;
       const int row = lane & 15;
-      // S^T = K Q^T, two chains of sums
+      // S^T = K Q^T, two chains of sums; fp32 q: a third for the parts below its
+      // first (the MMA cuts its sums, which costs least where they are small)
       float c[kSub][NT][4];
       auto scores = [&](auto parts) {
 #pragma unroll
         for (int u = 0; u < kSub; ++u) {
-          float c2[2][NT][4] = {};
+          float c2[QP > 1 ? 3 : 2][NT][4] = {};
           const uint32_t base = kt + (u * 16 + row) * Sh::kRow;
           if constexpr (BITS == 16) {
 #pragma unroll
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(32 * W, 1)
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int p = 0; p < decltype(parts)::value; ++p)
-                  mma(c2[k & 1][n], f[0], f[1], f[2], f[3], qf[p][n][k][0], qf[p][n][k][1]);
+                  mma(c2[p > 0 ? 2 : k & 1][n], f[0], f[1], f[2], f[3], qf[p][n][k][0], qf[p][n][k][1]);
             }
           } else {
 #pragma unroll
@@ -485,14 +486,17 @@ __global__ void __launch_bounds__(32 * W, 1)
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                   for (int p = 0; p < decltype(parts)::value; ++p)
-                    mma(c2[j][n], a0, a1, a2, a3, qf[p][n][k + j][0], qf[p][n][k + j][1]);
+                    mma(c2[p > 0 ? 2 : j][n], a0, a1, a2, a3, qf[p][n][k + j][0], qf[p][n][k + j][1]);
               }
             }
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[u][n][j] = c2[0][n][j] + c2[1][n][j];
+            for (int j = 0; j < 4; ++j) {
+              c[u][n][j] = c2[0][n][j] + c2[1][n][j];
+              if constexpr (QP > 1) c[u][n][j] += c2[2][n][j];
+            }
         }
       };
       scores(std::integral_constant<int, QP>());
@@ -573,9 +577,9 @@ __global__ void __launch_bounds__(32 * W, 1)
             }
           }
       }
+      uint32_t pf[kSub][QP][NT][2];
 #pragma unroll
-      for (int u = 0; u < kSub; ++u) {
-        uint32_t pf[QP][NT][2];
+      for (int u = 0; u < kSub; ++u)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float* x = c[u][n];
@@ -593,46 +597,68 @@ __global__ void __launch_bounds__(32 * W, 1)
           // tokens to the rows of the second product's right operand; bf16 q
           // rounds p to its own precision, fp32 q takes p whole
           if constexpr (QP == 1) {
-            pf[0][n][0] = movm_t(pack2(x[0], x[1]));
-            pf[0][n][1] = movm_t(pack2(x[2], x[3]));
+            pf[u][0][n][0] = movm_t(pack2(x[0], x[1]));
+            pf[u][0][n][1] = movm_t(pack2(x[2], x[3]));
           } else {
 #pragma unroll
             for (int p = 0; p < QP; ++p) {
-              pf[p][n][0] = movm_t(take2(x[0], x[1]));
-              pf[p][n][1] = movm_t(take2(x[2], x[3]));
+              pf[u][p][n][0] = movm_t(take2(x[0], x[1]));
+              pf[u][p][n][1] = movm_t(take2(x[2], x[3]));
             }
           }
         }
-        // O^T += V^T P^T
-        if constexpr (BITS == 16) {
-          // matrices: tokens 0-7 and 8-15 of values 0-7, then of values 8-15
-          const int vrow = (lane & 7) + (lane >> 4 & 1) * 8;
-          const uint32_t base = vt + (u * 16 + vrow) * Sh::kRow;
+      // O^T += V^T P^T.  fp32 q: a tile's sums are formed from zero, its first
+      // parts apart from the rest, and added to the output by fp32 additions,
+      // which round where the MMA cuts.
+      auto add = [&](int k, int u, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, float (&tile)[2][NT][4]) {
 #pragma unroll
-          for (int k = 0; k < kKs; ++k) {
-            uint32_t f[4];
-            ldsm4_t(base + piece_at<kChunks>(vrow, 2 * k + (lane >> 3 & 1)) * 16, f);
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (QP == 1) {
+            mma(o[k][n], a0, a1, a2, a3, pf[u][0][n][0], pf[u][0][n][1]);
+          } else {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int p = 0; p < QP; ++p) mma(o[k][n], f[0], f[1], f[2], f[3], pf[p][n][0], pf[p][n][1]);
+            for (int p = 0; p < QP; ++p)
+              mma(tile[p > 0][n], a0, a1, a2, a3, pf[u][p][n][0], pf[u][p][n][1]);
           }
-        } else {
-          const uint32_t base = vt + (u * 16 + row) * Sh::kRow;
+        }
+      };
+      auto settle = [&](int k, const float (&tile)[2][NT][4]) {
+        if constexpr (QP > 1) {
 #pragma unroll
-          for (int k = 0; k < kKs; k += 2) {
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[k][n][j] += tile[0][n][j] + tile[1][n][j];
+        }
+      };
+      if constexpr (BITS == 16) {
+        // matrices: tokens 0-7 and 8-15 of values 0-7, then of values 8-15
+        const int vrow = (lane & 7) + (lane >> 4 & 1) * 8;
+#pragma unroll
+        for (int k = 0; k < kKs; ++k) {
+          float tile[2][NT][4] = {};
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
             uint32_t f[4];
-            ldsm4_t(base + piece_at<kChunks>(row, k + (lane >> 4)) * 16, f);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t a0 = codes2(f[2 * j]), a1 = codes2(f[2 * j] >> 8);
-              const uint32_t a2 = codes2(f[2 * j + 1]), a3 = codes2(f[2 * j + 1] >> 8);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int p = 0; p < QP; ++p) mma(o[k + j][n], a0, a1, a2, a3, pf[p][n][0], pf[p][n][1]);
-            }
+            ldsm4_t(vt + (u * 16 + vrow) * Sh::kRow + piece_at<kChunks>(vrow, 2 * k + (lane >> 3 & 1)) * 16, f);
+            add(k, u, f[0], f[1], f[2], f[3], tile);
           }
+          settle(k, tile);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kKs; k += 2) {
+          float tile[2][2][NT][4] = {};
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            uint32_t f[4];
+            ldsm4_t(vt + (u * 16 + row) * Sh::kRow + piece_at<kChunks>(row, k + (lane >> 4)) * 16, f);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              add(k + j, u, codes2(f[2 * j]), codes2(f[2 * j] >> 8), codes2(f[2 * j + 1]),
+                  codes2(f[2 * j + 1] >> 8), tile[j]);
+          }
+          settle(k, tile[0]);
+          settle(k + 1, tile[1]);
         }
       }
 

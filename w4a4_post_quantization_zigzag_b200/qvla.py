@@ -9,6 +9,7 @@ has not been built (``python -m w4a4_post_quantization_zigzag_b200.build``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import (POINTER, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32,
                     c_void_p)
@@ -716,22 +717,25 @@ def _launch(fn, where: str, device: int, stream, *args):
     """fn(*args, stream) with `device` current; by default on its current stream."""
     if device < 0:
         raise ValueError(f"{where}: the tensors must be on a CUDA device")
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _launch(fn, where, device, stream, *args)
     if stream is None:
-        st = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        st = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    rc = fn(*args, st)
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    rc = fn(*args, stream)
     if rc != QVLA_OK:
         raise QvlaError(rc, where)
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
+def _empty(shape, dtype, device, stream, like: Optional[torch.Tensor] = None) -> torch.Tensor:
     """An output or scratch tensor whose memory belongs to the stream the
-    kernel runs on, so that its earlier and later uses there are in order."""
+    kernel runs on, so that its earlier and later uses there are in order.
+    like: a tensor of this shape, type and place, if there is one."""
     if stream is None:
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -777,7 +781,7 @@ def qvla_w4a16_gemv(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
     (default: x's)."""
     N, Kh = wq.shape
     K, groups = 2 * Kh, w_scale.shape[-1]
-    dev = x.get_device()
+    dev, dt = x.get_device(), out_dtype or x.dtype
     _expect_rows(x, K)
     _expect_on(wq, torch.uint8, (N, Kh), dev, "wq")
     _expect_on(w_scale, w_scale.dtype, (N, groups), dev, "w_scale")
@@ -788,21 +792,19 @@ def qvla_w4a16_gemv(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
     if bias is not None:
         _expect_on(bias, torch.float32, (N,), dev, "bias")
     M = x.shape[0]
+    pitch = (N + 7) // 8 * 8              # rows whose pitch is a multiple of 16 bytes
     if y is None:
-        # rows whose pitch is a multiple of 16 bytes
-        dt = out_dtype or x.dtype
-        y = _empty((M, (N + 7) // 8 * 8), dt, x.device, stream)
-        if N % 8:
+        y = _empty((M, pitch), dt, x.device, stream)
+        if N != pitch:
             y = y[:, :N]
-    elif (tuple(y.shape) != (M, N) or y.get_device() != dev or (y.numel() and y.stride(1) != 1)
-          or (out_dtype is not None and y.dtype != out_dtype)):
-        raise ValueError(f"y: expected [{M}, {N}] rows with unit stride on {x.device}")
+    elif (y.shape != (M, N) or y.get_device() != dev or (y.stride(1) != 1 and y.numel())
+          or (out_dtype is not None and y.dtype is not dt)):
+        raise ValueError(f"y: expected {dt} [{M}, {N}] rows with unit stride on {x.device}")
     L = qvla_group_linear(N, K, K // groups, _dtype_code(w_scale), wq.data_ptr(),
-                          w_scale.data_ptr(), None if w_zero is None else w_zero.data_ptr(),
-                          None if bias is None else bias.data_ptr())
+                          w_scale.data_ptr(), _address(w_zero), _address(bias))
     _launch(_lib.qvla_w4a16_gemv, "qvla_w4a16_gemv", dev, stream, x.data_ptr(), _dtype_code(x), M,
             x.stride(0) if M > 1 else K, L, y.data_ptr(), _dtype_code(y),
-            y.stride(0) if M > 1 else (N + 7) // 8 * 8)
+            y.stride(0) if M > 1 else pitch)
     return y
 
 
@@ -818,24 +820,22 @@ def qvla_rope_table(inv_freq, P: int, device="cuda", stream=None) -> torch.Tenso
     return table
 
 
-def _head_rows(x: torch.Tensor, device: int, dtype, name: str):
-    """[rows, heads, dim] with heads one after the other (any row pitch)."""
-    if x.dim() != 3 or x.dtype is not dtype or x.get_device() != device:
-        raise ValueError(f"{name}: expected a [rows, heads, dim] {dtype} tensor on cuda:{device}, "
-                         f"got {x.dtype} {tuple(x.shape)} on {x.device}")
-    T, H, D = x.shape
+def _head_rows(x: torch.Tensor, shape, device: int, dtype, name: str) -> int:
+    """The row pitch of [rows, heads, dim] whose heads lie one after the other."""
     st = x.stride()
-    if x.numel() and ((D > 1 and st[2] != 1) or (H > 1 and st[1] != D)):
-        raise ValueError(f"{name}: the heads of a row must lie one after the other, "
-                         f"got strides {tuple(st)}")
-    return st[0] if T > 1 else H * D
+    if (x.shape != shape or x.dtype is not dtype or x.get_device() != device
+            or ((st[2] != 1 or (st[1] != shape[2] and shape[1] > 1)) and x.numel())):
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} rows on cuda:{device} with the "
+                         f"heads one after the other, got {x.dtype} {tuple(x.shape)} with strides "
+                         f"{tuple(st)} on {x.device}")
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _kv_struct(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale, device: int):
     """The C cache of [pages, page_size, heads, dim] views in any memory order
     (bf16, or int8 with fp32 scales [pages, page_size, heads])."""
     shape, st, dt = k_cache.shape, k_cache.stride(), k_cache.dtype
-    if k_cache.dim() != 4 or (shape[3] > 1 and st[3] != 1):
+    if len(shape) != 4 or st[3] != 1:
         raise ValueError("k_cache: expected [pages, page_size, heads, dim] with unit stride "
                          f"along dim, got shape {tuple(shape)} strides {tuple(st)}")
     if v_cache.shape != shape or v_cache.stride() != st or v_cache.dtype is not dt:
@@ -846,7 +846,7 @@ def _kv_struct(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale, d
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale, v_scale: a bf16 cache has none")
         return qvla_kv_cache(*shape, 16, k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1],
-                             st[2], None, None, 0, 0, 0)
+                             st[2])
     if dt is not torch.int8:
         raise TypeError(f"unsupported cache dtype {dt}")
     for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
@@ -858,6 +858,10 @@ def _kv_struct(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale, d
         raise ValueError("v_scale: expected the strides of k_scale")
     return qvla_kv_cache(*shape, 8, k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2],
                          k_scale.data_ptr(), v_scale.data_ptr(), ss[0], ss[1], ss[2])
+
+
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def qvla_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
@@ -876,55 +880,52 @@ def qvla_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
     written to the cache slots `slots` (negative: not written).  Returns
     q_out; without a cache (q_out, k_out).  q_out / k_out may be q / k."""
     one = q if q is not None else k
-    if one is None:
-        raise ValueError("q, k: at least one is needed")
-    T, D, dt, dev = one.shape[0], one.shape[-1], one.dtype, one.get_device()
-    ldq = ldk = ldv = ldqo = ldko = 0
-    Hq = Hkv = 0
+    if one is None or one.dim() != 3:
+        raise ValueError("q, k: expected [T, heads, D] rows, at least one of them")
+    T, _, D = one.shape
+    dt, dev = one.dtype, one.get_device()
+    Hq = Hkv = ldq = ldk = ldv = ldqo = ldko = P = rot = 0
     if q is not None:
-        ldq, Hq = _head_rows(q, dev, dt, "q"), q.shape[1]
+        shape = q.shape
+        ldq, Hq = _head_rows(q, shape, dev, dt, "q"), shape[1]
         if q_out is None:
-            q_out = _empty((T, Hq, D), dt, q.device, stream)
-        ldqo = _head_rows(q_out, dev, dt, "q_out")
-        if q_out.shape != q.shape:
-            raise ValueError(f"q_out: expected shape {tuple(q.shape)}")
+            q_out = _empty(shape, dt, q.device, stream, q)
+        ldqo = _head_rows(q_out, shape, dev, dt, "q_out")
     if k is not None:
-        ldk, Hkv = _head_rows(k, dev, dt, "k"), k.shape[1]
-        if k.shape != (T, Hkv, D):
+        if k.dim() != 3:
             raise ValueError(f"k: expected [{T}, heads, {D}], got {tuple(k.shape)}")
+        shape = (T, k.shape[1], D)
+        ldk, Hkv = _head_rows(k, shape, dev, dt, "k"), shape[1]
         if k_out is None and k_cache is None:
-            k_out = _empty((T, Hkv, D), dt, k.device, stream)
+            k_out = _empty(shape, dt, k.device, stream, k)
         if k_out is not None:
-            ldko = _head_rows(k_out, dev, dt, "k_out")
-            if k_out.shape != k.shape:
-                raise ValueError(f"k_out: expected shape {tuple(k.shape)}")
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if w is not None:
-            _expect_on(w, torch.float32, (D,), dev, name)
-    P = rot = 0
+            ldko = _head_rows(k_out, shape, dev, dt, "k_out")
+    if q_norm is not None:
+        _expect_on(q_norm, torch.float32, (D,), dev, "q_norm")
+    if k_norm is not None:
+        _expect_on(k_norm, torch.float32, (D,), dev, "k_norm")
     if rope_table is not None:
+        if positions is None or rope_table.dim() != 2:
+            raise ValueError("rope_table: expected [positions, rot], and the tokens' positions")
         P, rot = rope_table.shape
         _expect_on(rope_table, torch.float32, (P, rot), dev, "rope_table")
-        if positions is None:
-            raise ValueError("positions: needed with rope_table")
         _expect_on(positions, torch.int32, (T,), dev, "positions")
     cache = None
     if k_cache is not None:
         if k is None or v is None or slots is None or v_cache is None:
             raise ValueError("a cache needs k, v, slots and v_cache")
-        ldv = _head_rows(v, dev, dt, "v")
-        if v.shape != k.shape:
-            raise ValueError(f"v: expected shape {tuple(k.shape)}")
+        ldv = _head_rows(v, (T, Hkv, D), dev, dt, "v")
         _expect_on(slots, torch.int32, (T,), dev, "slots")
         cache = _kv_struct(k_cache, v_cache, k_scale, v_scale, dev)
-    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _launch(_lib.qvla_qk_norm_rope, "qvla_qk_norm_rope", dev, stream, p(q), p(k),
-            p(v) if cache is not None else None, _dtype_code(one), T, Hq, Hkv, D, ldq, ldk, ldv,
-            p(q_norm), p(k_norm), eps, p(rope_table), P, rot, int(interleaved), p(positions),
-            cache, p(slots), p(q_out), ldqo, p(k_out), ldko)
+    _launch(_lib.qvla_qk_norm_rope, "qvla_qk_norm_rope", dev, stream, _address(q), _address(k),
+            _address(v), _dtype_code(one), T, Hq, Hkv, D, ldq, ldk, ldv, _address(q_norm),
+            _address(k_norm), eps, _address(rope_table), P, rot, int(interleaved),
+            _address(positions), cache, _address(slots), _address(q_out), ldqo, _address(k_out),
+            ldko)
     return q_out if cache is not None else (q_out, k_out)
 
 
+@functools.lru_cache(maxsize=256)
 def qvla_paged_attn_workspace_bytes(Hq: int, heads: int, dim: int) -> int:
     b = c_size_t()
     _check(_lib.qvla_paged_attn_workspace_bytes(Hq, heads, dim, ctypes.byref(b)),
@@ -942,32 +943,31 @@ def qvla_paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     cache; scale defaults to D ** -0.5.  lse: optional fp32 [B, Hq] output.
     workspace: uint8 device scratch of qvla_paged_attn_workspace_bytes()
     (allocated per call when None)."""
-    dt, dev = q.dtype, q.get_device()
-    ldq = _head_rows(q, dev, dt, "q")
-    B, Hq, D = q.shape
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [B, heads, D], got {tuple(q.shape)}")
+    shape, dt, dev = q.shape, q.dtype, q.get_device()
+    B, Hq, D = shape
+    ldq = _head_rows(q, shape, dev, dt, "q")
     cache = _kv_struct(k_cache, v_cache, k_scale, v_scale, dev)
     if cache.dim != D:
         raise ValueError(f"k_cache: expected dim {D}, got {cache.dim}")
     _expect_on(seq_lens, torch.int32, (B,), dev, "seq_lens")
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table: expected [{B}, pages], got {tuple(page_table.shape)}")
-    max_pages = page_table.shape[1]
+    max_pages = page_table.shape[-1]
     _expect_on(page_table, torch.int32, (B, max_pages), dev, "page_table")
     if out is None:
-        out = _empty((B, Hq, D), dt, q.device, stream)
-    elif out.shape != q.shape:
-        raise ValueError(f"out: expected shape {tuple(q.shape)}")
-    ldo = _head_rows(out, dev, dt, "out")
+        out = _empty(shape, dt, q.device, stream, q)
+    ldo = _head_rows(out, shape, dev, dt, "out")
     if lse is not None:
         _expect_on(lse, torch.float32, (B, Hq), dev, "lse")
     if workspace is None:
-        workspace = _empty(qvla_paged_attn_workspace_bytes(Hq, cache.heads, D), torch.uint8,
-                           q.device, stream)
+        ws_bytes = qvla_paged_attn_workspace_bytes(Hq, cache.heads, D)
+        workspace = _empty(ws_bytes, torch.uint8, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous memory on cuda:{dev}")
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
     _launch(_lib.qvla_paged_attn_decode, "qvla_paged_attn_decode", dev, stream, q.data_ptr(),
             _dtype_code(q), B, Hq, ldq, cache, page_table.data_ptr(), max_pages,
             seq_lens.data_ptr(), D ** -0.5 if scale is None else scale, window, sinks,
-            out.data_ptr(), ldo, None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+            out.data_ptr(), ldo, _address(lse), workspace.data_ptr(), ws_bytes)
     return out
