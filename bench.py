@@ -18,6 +18,11 @@ Besides the headline workload, the same line carries shorter measurements
 of the backbone prefill linears (1024 tokens, 2048<->16384) and of the full
 DiT denoise loop (512 tokens, 16 layers) under "secondary".
 
+`--workload backbone_decode` times one decode step of a backbone layer's
+attention half instead (one new token over a 1024-token prefix): the rotated
+W4A4 qkv linear, norm + rotation + cache write, attention over the paged
+cache, the W4A16 output projection, replayed from a CUDA graph.
+
 Prints one JSON line (rank 0).  `--impl reference` times the CPU oracle on the
 same workload instead (the reference arm: the pages publish no code to run).
 
@@ -46,8 +51,9 @@ from w4a4_post_quantization_zigzag_b200 import inputs as I  # noqa: E402
 METRIC = "µs per DiT denoise step"
 UNIT = "us/step"
 L2_FLUSH_BYTES = 512 << 20
+DECODE_METRIC = "µs per backbone decode step"
 WORKLOADS = ("dit_mlp_stack", "dit_mlp_stack_fused", "dit_denoise_loop",
-             "dit_denoise_loop_fused", "backbone_prefill", "single_linear")
+             "dit_denoise_loop_fused", "backbone_prefill", "single_linear", "backbone_decode")
 SECONDARY = ("backbone_prefill", "dit_denoise_loop")
 
 
@@ -593,6 +599,133 @@ def secondary_line(name, Q, dev, stream, steps, peaks):
     return r
 
 
+class DecodeStep:
+    """The attention half of one backbone layer for one new token per sequence
+    (Gemma-2B-like widths: 8 query heads of 256 on one key head), every part
+    of it an entry point of the library."""
+
+    def __init__(self, Q, dev, seed=6, batch=1, hidden=2048, Hq=8, Hkv=1, D=256, prefix=1024,
+                 page=16, block=128, group=128):
+        import torch
+        self.Q, self.shape = Q, (batch, hidden, Hq, Hkv, D, prefix)
+        dt = torch.bfloat16
+        up = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+        n_qkv = (Hq + 2 * Hkv) * D
+        self.qkv = Q.qvla_pack_weights(up(I.weights(seed, n_qkv, hidden)), block,
+                                       bias=up(I.bias(seed + 1, n_qkv)))
+        self.o = Q.qvla_pack_weights_w4g(up(I.weights(seed + 2, hidden, Hq * D)), group)
+        self.norms = [up(1 + I.bias(seed + 3 + i, D, std=0.1)) for i in range(2)]
+        self.table = Q.qvla_rope_table(10000.0 ** (-np.arange(0, D, 2) / D), prefix + 64,
+                                       device=dev)
+        self.x = up(I.activations(seed + 5, batch, hidden)).to(dt)
+        width = -(-(prefix + 1) // page)
+        pages = I.rng(seed + 6).permutation(batch * width).astype(np.int32).reshape(batch, width)
+        self.pages = up(pages)
+        kv = lambda s: up(I.activations(s, batch * width * page * Hkv, D)).to(dt).view(  # noqa: E731
+            batch * width, page, Hkv, D)
+        self.k_cache, self.v_cache = kv(seed + 7), kv(seed + 8)
+        self.positions = torch.full((batch,), prefix, dtype=torch.int32, device=dev)
+        self.slots = (self.pages[:, prefix // page] * page + prefix % page).contiguous()
+        self.lens = self.positions + 1
+        e = lambda *s, t=dt: torch.empty(*s, dtype=t, device=dev)  # noqa: E731
+        self.codes, self.s_x = e(batch, hidden // 2, t=torch.uint8), e(batch, t=torch.float32)
+        ws = Q.qvla_rotate_quant_workspace_bytes(batch, hidden, block)
+        self.rot_ws = e(max(ws, 16), t=torch.uint8)
+        self.attn_ws = e(Q.qvla_paged_attn_workspace_bytes(Hq, Hkv, D), t=torch.uint8)
+        self.rows, self.q = e(batch, n_qkv), e(batch, Hq, D)
+        self.attn, self.y = e(batch, Hq, D), e(batch, hidden)
+
+    def __call__(self):
+        Q, (batch, hidden, Hq, Hkv, D, _) = self.Q, self.shape
+        a, b = Hq * D, (Hq + Hkv) * D
+        Q.qvla_rotate_quant_act(self.x, self.qkv, xq=self.codes, s_x=self.s_x,
+                                workspace=self.rot_ws)
+        Q.qvla_w4a4_gemm(self.codes, self.s_x, self.qkv, y=self.rows)
+        Q.qvla_qk_norm_rope(self.rows[:, :a].unflatten(1, (Hq, D)),
+                            self.rows[:, a:b].unflatten(1, (Hkv, D)),
+                            self.rows[:, b:].unflatten(1, (Hkv, D)), *self.norms, self.table,
+                            self.positions, self.slots, self.k_cache, self.v_cache, q_out=self.q)
+        Q.qvla_paged_attn_decode(self.q, self.k_cache, self.v_cache, self.pages, self.lens,
+                                 out=self.attn, workspace=self.attn_ws)
+        Q.qvla_w4a16_gemv(self.attn.view(batch, a), *self.o, y=self.y)
+
+
+def run_decode(args):
+    """The backbone_decode workload on one GPU: one JSON line."""
+    import torch
+    if int(os.environ.get("WORLD_SIZE", "1")) != 1:
+        raise SystemExit("backbone_decode runs on one GPU")
+    from w4a4_post_quantization_zigzag_b200 import build as B
+    B.build()
+    from w4a4_post_quantization_zigzag_b200 import qvla as Q
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    step = DecodeStep(Q, dev)
+    stream = torch.cuda.Stream(device=dev)
+    flush = torch.empty(L2_FLUSH_BYTES // 4, dtype=torch.float32, device=dev)
+    x_host = step.x.cpu().pin_memory()
+    y_host = torch.empty_like(step.y, device="cpu").pin_memory()
+    ev = lambda: torch.cuda.Event(enable_timing=True)  # noqa: E731
+    with torch.cuda.stream(stream):
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph(keep_graph=True)
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+        launches = kernel_nodes(graph.raw_cuda_graph())
+        graph.instantiate()
+        marks = [(ev(), ev()) for _ in range(args.steps)]
+
+        def replay(i):
+            flush.zero_()
+            flush.sum()
+            if i >= 0:
+                marks[i][0].record()
+            graph.replay()
+            if i >= 0:
+                marks[i][1].record()
+
+        for _ in range(args.warmup):
+            replay(-1)
+        torch.cuda.synchronize()
+        sampler = ClockSampler("GPU-" + str(torch.cuda.get_device_properties(dev).uuid))
+        if not args.quick:
+            sampler.__enter__()
+        for i in range(args.steps):
+            replay(i)
+        torch.cuda.synchronize()
+        if not args.quick:
+            sampler.__exit__()
+        e0, e1 = ev(), ev()
+        e0.record()
+        for _ in range(args.steps):
+            step.x.copy_(x_host, non_blocking=True)
+            graph.replay()
+            y_host.copy_(step.y, non_blocking=True)
+        e1.record()
+        torch.cuda.synchronize()
+    assert Q.qvla_read_error_word(clear=True) == 0
+    us = sum(a.elapsed_time(b) for a, b in marks) / args.steps * 1e3
+    batch, hidden, Hq, Hkv, D, prefix = step.shape
+    line = {
+        "metric": DECODE_METRIC, "value": us, "unit": UNIT, "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": us / 1e3, "higher_is_better": False,
+        "scaling": "weak", "vs_baseline": None, "dtype": "s8/bf16", "data": "synthetic",
+        "config": {"workload": f"backbone_decode_B{batch}_d{hidden}_{Hq}x{Hkv}x{D}_prefix{prefix}",
+                   "l2": "flushed before every timed step (512 MB written, then read back: "
+                         "cold, clean L2)", "parallelism": "single"},
+        "gpu_launches": launches * args.steps, "kernels_per_step": launches,
+        "source_hash": Q.qvla_source_hash()[:16],
+        "e2e": {"value": e0.elapsed_time(e1) / args.steps * 1e3, "unit": UNIT,
+                "h2d_bytes_per_step": x_host.numel() * 2,
+                "d2h_bytes_per_step": y_host.numel() * 2},
+    }
+    if not args.quick:
+        line["clocks"] = sampler.summary()
+    del graph
+    print(json.dumps(line), flush=True)
+
+
 def run_ours(args):
     import torch
     import torch.distributed as dist
@@ -693,7 +826,13 @@ def run_ours(args):
 
 def main():
     args = parse()
-    if args.impl == "reference":
+    if args.workload == "backbone_decode":
+        if args.impl == "reference":
+            print(json.dumps({"impl": "reference",
+                              "unavailable": "the pages describe no decode step to run"}))
+        else:
+            run_decode(args)
+    elif args.impl == "reference":
         run_reference(args)
     else:
         run_ours(args)

@@ -106,3 +106,21 @@ def test_decode_loop(q, bits, window, linear):
             + torch.einsum("bht,bthd->bhd", p, step_v) * torch.exp(2 * ds)[..., None]
         R.within(at, dense, slack, "history")
     assert q.qvla_read_error_word(clear=True) == 0
+
+
+def test_bench_decode_workload():
+    """The bench's decode workload: one line, the whole step in the library's kernels (rotation,
+    its permuted copy, GEMM, norm, attention and its join, output projection)."""
+    import json
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "bench.py"), "--workload",
+                        "backbone_decode", "--steps", "4", "--warmup", "3", "--quick"], cwd=root,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    (line,) = [json.loads(l) for l in r.stdout.splitlines() if l.startswith("{")]
+    assert line["value"] > 0 and line["config"]["workload"].startswith("backbone_decode")
+    assert line["kernels_per_step"] >= 6 and line["gpu_launches"] == 4 * line["kernels_per_step"]
+    assert line["e2e"]["value"] > 0 and line["e2e"]["h2d_bytes_per_step"] == 2048 * 2
