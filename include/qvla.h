@@ -533,8 +533,8 @@ qvla_status qvla_pack_weights_w4g(const float* W, int N, int K, int group, qvla_
  * of 2^-22 (bf16) or 2^-29 (fp32) of the power of two at or below the largest
  * |x| of its group (an infinite or NaN activation makes its row NaN); for more
  * rows it enters whole.  A row's result does not depend on the other rows, nor
- * on M within M <= 2 and within M > 2.  M up to 2^20: the weights are read
- * again for every 16 rows, so many rows belong to qvla_w4a4_gemm().
+ * on M within M <= 2 and within M > 2.  M up to 65535 * 16: the weights are
+ * read again for every 16 rows, so many rows belong to qvla_w4a4_gemm().
  * Asynchronous, one launch, no workspace.                                   */
 qvla_status qvla_w4a16_gemv(const void* x, qvla_dtype xdt, int M, int ldx,
                             const qvla_group_linear* L, void* y, qvla_dtype ydt, int ldy,

@@ -77,6 +77,12 @@ def test_gemv(q):
     assert call(f, d, M=0, x=None, y=None) == q.QVLA_OK
 
 
+def test_gemv_rows_past_the_grid(q):
+    d = dict(x=P, xdt=1, M=65535 * 16 + 1, ldx=256, L=group_linear(q), y=P, ydt=1, ldy=128, stream=None)
+    assert call(q._lib.qvla_w4a16_gemv, d) == q.QVLA_ERR_SHAPE
+    assert call(q._lib.qvla_w4a16_gemv, d, M=1 << 20) == q.QVLA_ERR_SHAPE
+
+
 def test_rope_table(q):
     f = q._lib.qvla_rope_table
     d = dict(inv=P, half=32, P=100, table=P, stream=None)

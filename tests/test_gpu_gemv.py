@@ -66,6 +66,17 @@ def test_many_rows(q, M):
     check(q, rows(M, 512, F32), wq, s, z)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_most_rows(q, dt):
+    """As many rows as one grid takes; one more is refused."""
+    M = 65535 * 16
+    wq, s, _ = weights(8, 32, 32)
+    x = rows(M + 1, 32, dt)
+    check(q, x[:M], wq, s)
+    with pytest.raises(q.QvlaError):
+        q.qvla_w4a16_gemv(x, wq, s)
+
+
 @pytest.mark.parametrize("N,K,group,M", [(64, 16384, 128, 1), (100, 32768, 32, 2), (8200, 32768, 32, 1),
                                          (8200, 32768, 32, 3), (20000, 8192, 64, 2), (9000, 4096, 128, 9), (2048, 16384, 128, 3),
                                          (16384, 2048, 64, 1), (40, 32768, 256, 16),

@@ -21,6 +21,7 @@ size_t dtype_size(int d) { return d == QVLA_DTYPE_F32 ? 4 : 2; }
 bool aligned_pitch(int64_t elements, int d) { return elements * dtype_size(d) % 16 == 0; }
 
 constexpr int kMaxN = 1 << 22, kMaxRows = 1 << 20;
+constexpr int kMaxGemvRows = 65535 * 16;       // a grid's second extent, 16 rows a pass
 
 qvla_status check_group_shape(int N, int K, int group) {
   if (group != 32 && group != 64 && group != 128 && group != 256) return QVLA_ERR_SHAPE;
@@ -101,7 +102,7 @@ qvla_status qvla_w4a16_gemv(const void* x, qvla_dtype xdt, int M, int ldx,
   if (!L->wq || !L->w_scale) return QVLA_ERR_ARG;
   if (!aligned16(L->wq) || !aligned16(L->w_scale) || !aligned16(L->w_zero) || !aligned16(L->bias))
     return QVLA_ERR_ALIGN;
-  if (M < 0 || M > kMaxRows) return QVLA_ERR_SHAPE;
+  if (M < 0 || M > kMaxGemvRows) return QVLA_ERR_SHAPE;
   if (M == 0) return QVLA_OK;
   if (!x || !y) return QVLA_ERR_ARG;
   if (ldx < L->K || ldy < L->N) return QVLA_ERR_SHAPE;
