@@ -633,7 +633,7 @@ qvla_status qvla_qk_norm_rope(const void* q, const void* k, const void* v, qvla_
  * probabilities enter the second product as bf16, for fp32 q whole.  The
  * split of the work, and with it the order of the sums, depends on all
  * lengths of the call and is the same for equal calls.
- * Asynchronous, two launches.  B <= 2^16, B * Hq < 2^31.                    */
+ * Asynchronous, two launches.  B <= 2^16, max_pages * page_size <= 2^30.    */
 qvla_status qvla_paged_attn_decode(const void* q, qvla_dtype qdt, int B, int Hq, int ldq,
                                    const qvla_kv_cache* cache, const int32_t* page_table,
                                    int max_pages, const int32_t* seq_lens, float scale,

@@ -163,6 +163,15 @@ def test_paged_attn(q):
     assert call(f, d, B=0, q=None, table=None, lens=None, out=None, ws=None) == q.QVLA_OK
 
 
+def test_paged_attn_sequence_past_its_token_numbers(q):
+    """Pages may be shared, so a sequence's length is bounded by its table, not by the cache."""
+    need = q.qvla_paged_attn_workspace_bytes(8, 2, 64)
+    d = dict(q=P, qdt=1, B=3, Hq=8, ldq=512, cache=cache(q), table=P, max_pages=(1 << 26) + 1, lens=P, scale=0.125,
+             window=0, sinks=0, out=P, ldo=512, lse=P, ws=P, ws_bytes=need, stream=None)
+    assert call(q._lib.qvla_paged_attn_decode, d) == q.QVLA_ERR_SHAPE
+    assert call(q._lib.qvla_paged_attn_decode, d, max_pages=(1 << 27) - 1) == q.QVLA_ERR_SHAPE
+
+
 def test_binding_refuses_host_and_mismatched_tensors(q):
     """Wrong types, shapes and places raise in the binding; nothing of them reaches a kernel."""
     x, wq, s = torch.zeros(2, 128), torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 4)

@@ -227,8 +227,8 @@ qvla_status qvla_paged_attn_decode(const void* q, qvla_dtype qdt, int B, int Hq,
   if ((st = qvla_paged_attn_workspace_bytes(Hq, cache->heads, cache->dim, &need)) != QVLA_OK)
     return st;
   if (B < 0 || B > 65536 || max_pages <= 0) return QVLA_ERR_SHAPE;
-  // a sequence's token numbers are 32 bits wide
-  if (static_cast<int64_t>(max_pages) * cache->page_size > INT_MAX) return QVLA_ERR_SHAPE;
+  // a sequence's token numbers, rounded up to whole tiles, are 32 bits wide
+  if (static_cast<int64_t>(max_pages) * cache->page_size > (1 << 30)) return QVLA_ERR_SHAPE;
   if (B == 0) return QVLA_OK;
   if (!q || !page_table || !seq_lens || !out) return QVLA_ERR_ARG;
   const int64_t row = static_cast<int64_t>(Hq) * cache->dim;
