@@ -135,6 +135,17 @@ def test_qk_norm_rope(q):
     assert call(f, d, T=0, q=None, k=None, v=None, pos=None, slots=None, q_out=None) == q.QVLA_OK
 
 
+def test_qk_norm_rope_in_place_with_another_pitch(q):
+    """Rows written at another pitch over their own inputs would overwrite rows not yet read."""
+    Q, O = ctypes.c_void_p(1 << 21), ctypes.c_void_p(1 << 22)
+    d = dict(q=Q, k=P, v=P, xdt=1, T=4, Hq=8, Hkv=2, D=64, ldq=768, ldk=768, ldv=768, qn=P, kn=P, eps=1e-6,
+             table=P, P=100, rot=64, inter=0, pos=P, cache=cache(q), slots=P, q_out=O, ldqo=512, k_out=O,
+             ldko=128, stream=None)
+    f = q._lib.qvla_qk_norm_rope
+    assert call(f, d, q_out=Q) == q.QVLA_ERR_ARG
+    assert call(f, d, k_out=P) == q.QVLA_ERR_ARG
+
+
 def test_paged_attn(q):
     b = ctypes.c_size_t()
     g = q._lib.qvla_paged_attn_workspace_bytes

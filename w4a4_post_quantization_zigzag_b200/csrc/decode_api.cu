@@ -175,6 +175,9 @@ qvla_status qvla_qk_norm_rope(const void* q, const void* k, const void* v, qvla_
       (Hkv && (!aligned_pitch(ldk, xdt) || (cache && !aligned_pitch(ldv, xdt)) ||
                (k_out && !aligned_pitch(ldko, xdt)))))
     return QVLA_ERR_ALIGN;
+  // in place, a row may only be written where it was read
+  if (T > 1 && ((Hq && q == q_out && ldq != ldqo) || (Hkv && k == k_out && ldk != ldko)))
+    return QVLA_ERR_ARG;
   if ((st = check_sm100()) != QVLA_OK) return st;
   NormRopeArgs a = {};
   a.q = q;
