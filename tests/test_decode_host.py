@@ -183,6 +183,32 @@ def test_paged_attn_sequence_past_its_token_numbers(q):
     assert call(q._lib.qvla_paged_attn_decode, d, max_pages=(1 << 27) - 1) == q.QVLA_ERR_SHAPE
 
 
+def test_binding_refuses_what_32_bits_do_not_hold(q):
+    """Pitches, windows and sizes past 32 bits must not reach the C call cut to their low bits."""
+    def meta(shape, strides=None, dt=torch.bfloat16):
+        if strides is None:
+            return torch.empty(shape, dtype=dt, device="meta")
+        return torch.empty_strided(shape, strides, dtype=dt, device="meta")
+    far = (1 << 32) + 128
+    wq, s = meta((128, 64), dt=torch.uint8), meta((128, 4))
+    x, i32 = meta((2, 128)), dict(dt=torch.int32)
+    h, kc = meta((2, 4, 16)), meta((5, 8, 4, 16))
+    tab, lens = meta((2, 3), **i32), meta((2,), **i32)
+    calls = [lambda: q.qvla_w4a16_gemv(meta((2, 128), (far, 1)), wq, s),
+             lambda: q.qvla_w4a16_gemv(x, wq, s, y=meta((2, 128), (far, 1))),
+             lambda: q.qvla_qk_norm_rope(meta((2, 4, 16), (far, 16, 1)), None),
+             lambda: q.qvla_qk_norm_rope(h, None, q_out=meta((2, 4, 16), (far, 16, 1))),
+             lambda: q.qvla_qk_norm_rope(h, None, rope_table=meta((1 << 31, 16), dt=torch.float32),
+                                         positions=meta((2,), **i32)),
+             lambda: q.qvla_paged_attn_decode(h, kc, kc, tab, lens, window=(1 << 32) + 5),
+             lambda: q.qvla_paged_attn_decode(h, kc, kc, tab, lens, window=5, sinks=1 << 32),
+             lambda: q.qvla_paged_attn_decode(h, kc, kc, tab, lens, window=-1),
+             lambda: q.qvla_paged_attn_decode(h, meta((far, 8, 4, 16)), meta((far, 8, 4, 16)), tab, lens)]
+    for f in calls:
+        with pytest.raises(q.QvlaError):
+            f()
+
+
 def test_binding_refuses_host_and_mismatched_tensors(q):
     """Wrong types, shapes and places raise in the binding; nothing of them reaches a kernel."""
     x, wq, s = torch.zeros(2, 128), torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 4)

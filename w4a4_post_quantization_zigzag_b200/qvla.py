@@ -792,6 +792,8 @@ def qvla_w4a16_gemv(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
     if bias is not None:
         _expect_on(bias, torch.float32, (N,), dev, "bias")
     M = x.shape[0]
+    ldx = x.stride(0) if M > 1 else K
+    _expect_int32("x", M | ldx)
     pitch = (N + 7) // 8 * 8              # rows whose pitch is a multiple of 16 bytes
     if y is None:
         y = _empty((M, pitch), dt, x.device, stream)
@@ -800,11 +802,12 @@ def qvla_w4a16_gemv(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
     elif (y.shape != (M, N) or y.get_device() != dev or (y.stride(1) != 1 and y.numel())
           or (out_dtype is not None and y.dtype is not dt)):
         raise ValueError(f"y: expected {dt} [{M}, {N}] rows with unit stride on {x.device}")
+    ldy = y.stride(0) if M > 1 else pitch
+    _expect_int32("y", ldy)
     L = qvla_group_linear(N, K, K // groups, _dtype_code(w_scale), wq.data_ptr(),
                           w_scale.data_ptr(), _address(w_zero), _address(bias))
     _launch(_lib.qvla_w4a16_gemv, "qvla_w4a16_gemv", dev, stream, x.data_ptr(), _dtype_code(x), M,
-            x.stride(0) if M > 1 else K, L, y.data_ptr(), _dtype_code(y),
-            y.stride(0) if M > 1 else pitch)
+            ldx, L, y.data_ptr(), _dtype_code(y), ldy)
     return y
 
 
@@ -820,6 +823,12 @@ def qvla_rope_table(inv_freq, P: int, device="cuda", stream=None) -> torch.Tenso
     return table
 
 
+def _expect_int32(where: str, bits: int):
+    """bits: sizes, or their bitwise or, that the C call takes as 32-bit integers."""
+    if bits >> 31:
+        raise QvlaError(QVLA_ERR_SHAPE, where)
+
+
 def _head_rows(x: torch.Tensor, shape, device: int, dtype, name: str) -> int:
     """The row pitch of [rows, heads, dim] whose heads lie one after the other."""
     st = x.stride()
@@ -828,7 +837,10 @@ def _head_rows(x: torch.Tensor, shape, device: int, dtype, name: str) -> int:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} rows on cuda:{device} with the "
                          f"heads one after the other, got {x.dtype} {tuple(x.shape)} with strides "
                          f"{tuple(st)} on {x.device}")
-    return st[0] if shape[0] > 1 else shape[1] * shape[2]
+    if shape[0] <= 1:
+        return shape[1] * shape[2]
+    _expect_int32(name, st[0] | shape[0])
+    return st[0]
 
 
 def _kv_struct(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale, device: int):
@@ -840,6 +852,7 @@ def _kv_struct(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale, d
                          f"along dim, got shape {tuple(shape)} strides {tuple(st)}")
     if v_cache.shape != shape or v_cache.stride() != st or v_cache.dtype is not dt:
         raise ValueError("v_cache: expected the shape, strides and type of k_cache")
+    _expect_int32("k_cache", shape[0] | shape[1])
     if k_cache.get_device() != device or v_cache.get_device() != device:
         raise ValueError(f"k_cache, v_cache: expected them on cuda:{device}")
     if dt is torch.bfloat16:
@@ -908,6 +921,7 @@ def qvla_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
         if positions is None or rope_table.dim() != 2:
             raise ValueError("rope_table: expected [positions, rot], and the tokens' positions")
         P, rot = rope_table.shape
+        _expect_int32("rope_table", P)
         _expect_on(rope_table, torch.float32, (P, rot), dev, "rope_table")
         _expect_on(positions, torch.int32, (T,), dev, "positions")
     cache = None
@@ -953,6 +967,7 @@ def qvla_paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
         raise ValueError(f"k_cache: expected dim {D}, got {cache.dim}")
     _expect_on(seq_lens, torch.int32, (B,), dev, "seq_lens")
     max_pages = page_table.shape[-1]
+    _expect_int32("window, sinks, max_pages", window | sinks | max_pages)
     _expect_on(page_table, torch.int32, (B, max_pages), dev, "page_table")
     if out is None:
         out = _empty(shape, dt, q.device, stream, q)
