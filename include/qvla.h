@@ -528,14 +528,15 @@ qvla_status qvla_pack_weights_w4g(const float* W, int N, int K, int group, qvla_
                                   cudaStream_t stream);
 
 /* y = x W^T + b for few rows of x.  x device [M][ldx] of xdt, y device
- * [M][ldy] of ydt (ldx >= K, ldy >= N).  Sums are fp32 or wider; y is rounded
- * once.  For one and two rows, each activation enters as an integer multiple
- * of 2^-22 (bf16) or 2^-29 (fp32) of the power of two at or below the largest
- * |x| of its group (an infinite or NaN activation makes its row NaN); for more
- * rows it enters whole.  A row's result does not depend on the other rows, nor
- * on M within M <= 2 and within M > 2.  M up to 65535 * 16: the weights are
- * read again for every 16 rows, so many rows belong to qvla_w4a4_gemm().
- * Asynchronous, one launch, no workspace.                                   */
+ * [M][ldy] of ydt (ldx >= K, ldy >= N), apart from x.  Sums are fp32 or
+ * wider; y is rounded once.  For one and two rows, each activation enters as
+ * an integer multiple of 2^-22 (bf16) or 2^-29 (fp32) of the power of two at
+ * or below the largest |x| of its group (an infinite or NaN activation makes
+ * its row NaN); for more rows it enters whole (an infinite fp32 one as NaN).
+ * A row's result does not depend on the other rows, nor on M within M <= 2 and
+ * within M > 2.  M up to 65535 * 16: the weights are read again for every 16
+ * rows, so many rows belong to qvla_w4a4_gemm().  Asynchronous, one launch, no
+ * workspace.                                                                */
 qvla_status qvla_w4a16_gemv(const void* x, qvla_dtype xdt, int M, int ldx,
                             const qvla_group_linear* L, void* y, qvla_dtype ydt, int ldy,
                             cudaStream_t stream);
@@ -620,9 +621,9 @@ qvla_status qvla_qk_norm_rope(const void* q, const void* k, const void* v, qvla_
  *           among them.  0 gives o = 0 and lse = -inf.
  * window, sinks  window 0: every token is visible.  Else the last `window`
  *           tokens and the first `sinks` are.  Hidden tokens are not read.
- * out       device [B][ldo] of qdt.  lse device fp32 [B][Hq] or NULL: the
- *           natural logarithm of the sum of exponentials (to join this result
- *           with attention over other keys).
+ * out       device [B][ldo] of qdt; may be q itself (same pitch).
+ * lse       device fp32 [B][Hq] or NULL: the natural logarithm of the sum of
+ *           exponentials (to join this result with attention over other keys).
  * workspace device, >= qvla_paged_attn_workspace_bytes(); its contents need
  *           not start at anything and mean nothing afterwards.  Calls (or
  *           graphs) that may run at the same time need one each.

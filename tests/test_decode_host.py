@@ -183,6 +183,13 @@ def test_paged_attn_sequence_past_its_token_numbers(q):
     assert call(q._lib.qvla_paged_attn_decode, d, max_pages=(1 << 27) - 1) == q.QVLA_ERR_SHAPE
 
 
+def test_paged_attn_in_place_with_another_pitch(q):
+    need = q.qvla_paged_attn_workspace_bytes(8, 2, 64)
+    d = dict(q=P, qdt=1, B=3, Hq=8, ldq=768, cache=cache(q), table=P, max_pages=10, lens=P, scale=0.125, window=0,
+             sinks=0, out=P, ldo=512, lse=P, ws=P, ws_bytes=need, stream=None)
+    assert call(q._lib.qvla_paged_attn_decode, d) == q.QVLA_ERR_ARG
+
+
 def test_binding_refuses_what_32_bits_do_not_hold(q):
     """Pitches, windows and sizes past 32 bits must not reach the C call cut to their low bits."""
     def meta(shape, strides=None, dt=torch.bfloat16):

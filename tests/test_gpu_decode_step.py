@@ -2,6 +2,10 @@
 qkv linear, norm + rotation + cache write, attention over the cache, a W4A16 output projection,
 captured once and replayed for every new token.  Each stage is held to fp64 of its own inputs, and
 the attention to a dense history kept beside the cache."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -10,6 +14,7 @@ import _decode_ref as R
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
 EPS = 1e-6
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -108,16 +113,47 @@ def test_decode_loop(q, bits, window, linear):
     assert q.qvla_read_error_word(clear=True) == 0
 
 
+def test_first_calls_inside_a_capture():
+    """Every operator's first call of a process may be the captured one."""
+    code = '''
+import torch
+from w4a4_post_quantization_zigzag_b200 import qvla as q
+dev, BF = "cuda", torch.bfloat16
+x = torch.randn(3, 256, device=dev).to(BF)
+W = torch.randn(64, 256, device=dev)
+h = torch.randn(2, 6, 64, device=dev).to(BF)
+kc, vc = (torch.zeros(4, 16, 2, 64, device=dev, dtype=BF) for _ in range(2))
+i32 = dict(dtype=torch.int32, device=dev)
+pos, slots = torch.tensor([3, 0], **i32), torch.tensor([3, 16], **i32)
+tab, lens = torch.tensor([[0], [1]], **i32), torch.tensor([4, 1], **i32)
+freqs = [10000.0 ** (-i / 32) for i in range(32)]
+def step():
+    wq, s, z = q.qvla_pack_weights_w4g(W, 64, True)
+    table = q.qvla_rope_table(freqs, 8)
+    out = q.qvla_qk_norm_rope(h[:, :4], h[:, 4:], h[:, 4:], None, None, table, pos, slots, kc, vc)
+    return (q.qvla_w4a16_gemv(x, wq, s, z), q.qvla_w4a16_gemv(x[:1], wq, s, z), out,
+            q.qvla_paged_attn_decode(out, kc, vc, tab, lens))
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+torch.cuda.synchronize()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert q.qvla_read_error_word() == 0
+'''
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_bench_decode_workload():
     """The bench's decode workload: one line, the whole step in the library's kernels (rotation,
     its permuted copy, GEMM, norm, attention and its join, output projection)."""
     import json
-    import os
-    import subprocess
-    import sys
-    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    r = subprocess.run([sys.executable, os.path.join(root, "bench.py"), "--workload",
-                        "backbone_decode", "--steps", "4", "--warmup", "3", "--quick"], cwd=root,
+    r = subprocess.run([sys.executable, os.path.join(ROOT, "bench.py"), "--workload",
+                        "backbone_decode", "--steps", "4", "--warmup", "3", "--quick"], cwd=ROOT,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     (line,) = [json.loads(l) for l in r.stdout.splitlines() if l.startswith("{")]

@@ -232,6 +232,37 @@ def test_graph_and_side_stream(q):
     assert torch.equal(other, y)
 
 
+@pytest.mark.parametrize("N,K,M", [(40, 16384, 1), (40, 16384, 5), (200, 2048, 2), (9000, 512, 16)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_graphs_at_the_same_time(q, N, K, M, dt):
+    """The split over a cluster included: calls share nothing, so graphs may run side by side."""
+    wq, s, z = weights(N, K, 128, zero=True)
+    x = rows(M, K, dt)
+    want = check(q, x, wq, s, z)
+    torch.cuda.synchronize()
+    ys, graphs = [], []
+    for _ in range(2):
+        y = torch.empty(M, (N + 7) // 8 * 8, dtype=dt, device="cuda")[:, :N]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(3):
+                q.qvla_w4a16_gemv(x, wq, s, z, y=y)
+        ys.append(y)
+        graphs.append(g)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        for y in ys:
+            y.zero_()
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        eager = q.qvla_w4a16_gemv(x, wq, s, z)
+        torch.cuda.synchronize()
+        for y in (*ys, eager):
+            assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("group", [32, 64, 128, 256])
 @pytest.mark.parametrize("sdt", [F32, BF])
 @pytest.mark.parametrize("zero", [False, True])

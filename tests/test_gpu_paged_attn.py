@@ -189,6 +189,16 @@ def test_pitches_given_output_and_workspace(q):
         assert (buf[:, :256] == 7).all() and (buf[:, 768:] == 7).all()
 
 
+@pytest.mark.parametrize("lens", [[700], [3, 900, 0, 40, 16], [20] * 64])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_in_place(q, lens, dt):
+    """out may be q: a row's last reader is done before it is written, however it is split."""
+    d = setup(lens, 24, 2, 64, dt)
+    want = check(q, d)
+    assert run(q, d, out=d["q"]) is d["q"]
+    assert torch.equal(d["q"], want)
+
+
 def test_shared_pages_and_equal_calls(q):
     """Sequences may share pages; equal calls give equal bits."""
     d = setup([200, 200], 8, 2, 64)

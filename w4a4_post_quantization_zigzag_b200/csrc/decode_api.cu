@@ -239,6 +239,7 @@ qvla_status qvla_paged_attn_decode(const void* q, qvla_dtype qdt, int B, int Hq,
   if (!aligned16(q) || !aligned16(out) || !aligned_pitch(ldq, qdt) || !aligned_pitch(ldo, qdt) ||
       !aligned4(page_table) || !aligned4(seq_lens) || !aligned4(lse))
     return QVLA_ERR_ALIGN;
+  if (B > 1 && q == out && ldq != ldo) return QVLA_ERR_ARG;      // in place, row on row only
   if (!workspace || ws_bytes < need) return QVLA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QVLA_ERR_ALIGN;
   if ((st = check_sm100()) != QVLA_OK) return st;
