@@ -63,10 +63,15 @@ __global__ void __launch_bounds__(256) pack_w4g_kernel(const float* __restrict__
 // Bound by reading the codes once, so the work per code has to be small.  Two
 // kernels share the way the codes come and how work is dealt; one multiplies
 // in integers and serves one and two activation rows, the other in bf16 and
-// serves more.  (Per 32 x 256 codes the integer kernel spends about 230
-// warp instructions on the codes and 27 per row, the bf16 kernel 470 and 13.
-// 2048 -> 131072, groups of 128: one row 24.9 against 34.3 us, eight rows 42
-// against 39 us; 4096 -> 1024, eight rows: 8.5 against 4.1 us.)
+// serves more.  (2048 -> 131072, groups of 128: one row 25.6 us in integers,
+// 5.4 TB/s, against 37.7 in bf16, two rows 26.0 against 37.8, three, which
+// would be two passes in integers, 51 against 38; sixteen rows 56.5 us.  1536
+// -> 6144, groups of 32, fp32: one row 6.0 against 7.8 us.  Where the codes
+// fit the SMs at once there is little between them: 4096 -> 4096, one row 5.6
+// against 5.4 us.)  One and two rows of a large matrix are bound by memory
+// (85 % of the copy rate); more rows by the warps' instructions, about 900 per
+// 32 x 256 codes at sixteen rows, half of them to expand the codes; small
+// matrices by the launch and one trip to memory (1024 -> 4096: 3.8 us).
 //
 // A warp multiplies bands of 32 weight rows.  A CTA has WR x WK warps: WR
 // groups that take bands in turn, K dealt to the WK warps of a group in chunks
@@ -976,7 +981,7 @@ cudaError_t launch_gemv(K kernel, std::atomic<unsigned long long>& done, const G
 // Gives up ring stages, then bands at a time (neither changes a result), until
 // `bytes` of shared memory fit; then the third stage, where without it more
 // CTAs are on an SM at once and there are CTAs for them (16384 -> 2048, one
-// row: 8.1 against 13.5 us).
+// row: 8.2 against 13.6 us).
 template <typename F>
 bool make_fit(GemvShape& sh, int N, int sms, F bytes) {
   while (bytes(sh) > kMaxSmem) {
@@ -1014,9 +1019,10 @@ template <int G, int MT, int XP>
 cudaError_t run_parts(const GemvArgs& a, GemvShape sh, int sms, cudaStream_t stream) {
   sh.rows = std::min(a.M, 8 * MT);
   // Operand order is worth its staging where warps take several bands
-  // (2048 -> 131072, 16 rows: 53.6 against 60.8 us) or the activations have to
-  // be split (1536 -> 6144, seven fp32 rows: 8.6 against 9.8 us), and the
-  // activations leave room for rings of two stages.
+  // (2048 -> 131072, 16 rows: 56.5 against 67.5 us, 8 rows: 39.2 against 51.9)
+  // or the activations have to be split (1536 -> 6144, seven fp32 rows: 9.6
+  // against 12.2 us), and the activations leave room for rings of two stages.
+  // With one band a warp it changes nothing (4096 -> 4096, 16 rows: 8.2).
   GemvShape st = sh;
   if (sh.KC == 1 && (XP > 1 || wanted_ctas(sh, a.N) > sms)) {
     auto bytes = [&](const GemvShape& s) { return part_layout(s, a.K, XP, true).bytes; };

@@ -21,6 +21,12 @@
 //
 // Each warp feeds itself: cp.async of its own tiles into its own ring of
 // shared memory, no barrier with other warps before the join.
+//
+// One sequence of 131072 tokens, 32 over 8 heads of 128: 93 us, 5.8 TB/s (88 %
+// of the copy rate); 32 sequences of up to 8192: 91 us.  With little to read
+// the time is a chain of waits (lengths, page numbers, first tiles, the join,
+// the second launch): 13.6 us at 1040 tokens and 8 over 1 heads of 256, 27.7
+// at 64 sequences that see 2000 tokens in 8 bits (5 us of bytes).
 #include "qvla_common.cuh"
 #include "qvla_internal.h"
 

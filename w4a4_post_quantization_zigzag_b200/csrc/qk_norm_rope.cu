@@ -259,7 +259,10 @@ constexpr int kResident = 2;
 // j + rot/16 of the row), so norm, rotation and stores need no exchange but the
 // sum of squares (and the maximum, for 8-bit codes).  A lane writes only what it
 // read, so q_out and k_out may be the inputs.  The next pass's rows are loaded
-// before this pass's are worked on.
+// before this pass's are worked on.  16381 tokens of 32 + 8 + 8 heads of 128:
+// 85 us for 411 MB read and written, 4.8 TB/s (73 % of the copy rate of large
+// buffers; a plain device copy of 206 MB ran at 3.0).  1024 tokens of 8 + 1 + 1
+// heads of 256: 5.0 us, one token 2.4: the launch and one trip to memory.
 template <typename X, int LPR, bool INTER>
 __global__ void __launch_bounds__(256, kResident)
     norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ RowShare sh,
