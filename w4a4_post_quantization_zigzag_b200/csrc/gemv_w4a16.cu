@@ -788,8 +788,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     xrow[n] = static_cast<const X*>(a.x) + static_cast<int64_t>(m0 + xcol[n]) * a.ldx + t * 8 * kWords;
   }
   if constexpr (STAGED) {
-    // 16-byte pieces in the order the lanes read them: [segment, word, part][t]
-    // [column]
+    // 16-byte pieces in the order the lanes read them: [segment, word, part]
+    // [column][t], so that the eight lanes of a quarter warp meet no bank twice
     const int pieces = a.K / 8;
     for (int i = threadIdx.x; i < pieces * cols; i += blockDim.x) {
       const int k8 = i % pieces, col = i / pieces;
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
           load_acts<XP>(static_cast<const X*>(a.x) + static_cast<int64_t>(m0 + col) * a.ldx + k8 * 8);
 #pragma unroll
       for (int p = 0; p < XP; ++p)
-        xs[((((seg * kWords + q % kWords) * XP + p) * 4 + q / kWords)) * cols + col] =
+        xs[(((seg * kWords + q % kWords) * XP + p) * cols + col) * 4 + q / kWords] =
             make_uint4(v.p[p][0], v.p[p][1], v.p[p][2], v.p[p][3]);
     }
     __syncthreads();
@@ -841,10 +841,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
           for (int n = 0; n < MT; ++n) {
             Acts<XP> b;
             if constexpr (STAGED) {
-              const int piece = ((c * kSegs + seg) * kWords + j) * XP * 4 + t;
+              const int piece = ((c * kSegs + seg) * kWords + j) * XP;
 #pragma unroll
               for (int p = 0; p < XP; ++p) {
-                const uint4 v = xs[(piece + p * 4) * cols + xcol[n]];
+                const uint4 v = xs[((piece + p) * cols + xcol[n]) * 4 + t];
                 b.p[p][0] = v.x, b.p[p][1] = v.y, b.p[p][2] = v.z, b.p[p][3] = v.w;
               }
             } else {
