@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
         load_next((band + w.band_step) * 32 + lane, w.first);
       const uint32_t stage = smem_u32(ring.mem) + ring.stage * kStageBytes;
       // two chains of sums; fp32 x: its first part apart from the rest
-      float part[2][2][MT][4];
+      float part[XP == 1 ? 1 : 2][2][MT][4];
 #pragma unroll
       for (int seg = 0; seg < kSegs; ++seg) {
         if (c * kChunk + seg * kSeg >= a.K) break;
@@ -854,8 +854,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
             for (int p = 0; p < XP; ++p)
 #pragma unroll
               for (int d = 0; d < 2; ++d) {              // the word's two MMAs
-                const int q = XP == 1 ? d : p > 0;
-                const bool opens = seg * kSeg % G == 0 && j == 0 && (XP == 1 || (d == 0 && p < 2));
+                const int q = p > 0;
+                const bool opens = seg * kSeg % G == 0 && j == 0 && d == 0 && p < 2;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   if (opens)
@@ -874,7 +874,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
             const float s0 = __shfl_sync(0xffffffffu, rg.s[grp], rho + 16 * h);
             const float s1 = __shfl_sync(0xffffffffu, rg.s[grp], rho + 16 * h + 8);
 #pragma unroll
-            for (int q = 1; q >= 0; --q)
+            for (int q = XP > 1; q >= 0; --q)
 #pragma unroll
               for (int n = 0; n < MT; ++n)
 #pragma unroll
