@@ -210,12 +210,14 @@ QVLA_DEVICE void load_codes(uint32_t stage, int seg, int rho, int t, uint32_t (&
   }
 }
 
-QVLA_DEVICE float scale_at(const GemvArgs& a, int64_t i) {
-  return a.sdt == QVLA_DTYPE_F32 ? static_cast<const float*>(a.scale)[i]
-                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(a.scale)[i]);
-}
-
-// Scales and zero points of one row's chunk.
+// Scales and zero points of one row's chunk, as they lie in memory: loaded a
+// chunk ahead and converted where they are used, so that no warp waits for the
+// load itself.
+template <int NG>
+struct RawGroups {
+  uint32_t s[NG];            // fp32 bits, or bf16 two to a word
+  uint32_t z[(NG + 3) / 4];  // bytes
+};
 template <int NG>
 struct RowGroups {
   float s[NG];
@@ -223,66 +225,78 @@ struct RowGroups {
 };
 
 template <int NG, bool ZERO>
-QVLA_DEVICE void load_groups(const GemvArgs& a, int n, int c, RowGroups<NG>& r) {
+QVLA_DEVICE void load_groups(const GemvArgs& a, int n, int c, RawGroups<NG>& r) {
   const int groups = a.K / a.group;
   const int64_t at = static_cast<int64_t>(n) * groups + c * NG;
   if (groups % NG == 0) {
     // every row's chunk is whole and starts at a multiple of its size
     if (a.sdt == QVLA_DTYPE_F32) {
-      const float* p = static_cast<const float*>(a.scale) + at;
+      const uint32_t* p = static_cast<const uint32_t*>(a.scale) + at;
       if constexpr (NG >= 4) {
 #pragma unroll
         for (int j = 0; j < NG; j += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(p + j);
+          const uint4 v = *reinterpret_cast<const uint4*>(p + j);
           r.s[j] = v.x, r.s[j + 1] = v.y, r.s[j + 2] = v.z, r.s[j + 3] = v.w;
         }
       } else if constexpr (NG == 2) {
-        const float2 v = *reinterpret_cast<const float2*>(p);
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
         r.s[0] = v.x, r.s[1] = v.y;
       } else {
         r.s[0] = *p;
       }
     } else {
-      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.scale) + at;
-      if constexpr (NG >= 2) {
-        uint32_t w[NG / 2];
-        if constexpr (NG == 8)
-          *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
-        else if constexpr (NG == 4)
-          *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
-        else
-          w[0] = *reinterpret_cast<const uint32_t*>(p);
-#pragma unroll
-        for (int j = 0; j < NG / 2; ++j) {
-          r.s[2 * j] = __uint_as_float(w[j] << 16);
-          r.s[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
+      const uint16_t* p = static_cast<const uint16_t*>(a.scale) + at;
+      if constexpr (NG == 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        r.s[0] = v.x, r.s[1] = v.y, r.s[2] = v.z, r.s[3] = v.w;
+      } else if constexpr (NG == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        r.s[0] = v.x, r.s[1] = v.y;
+      } else if constexpr (NG == 2) {
+        r.s[0] = *reinterpret_cast<const uint32_t*>(p);
       } else {
-        r.s[0] = __bfloat162float(*p);
+        r.s[0] = *p;
       }
     }
     if constexpr (ZERO) {
       const uint8_t* p = a.zero + at;
-      uint32_t w[2] = {0u, 0u};
-      if constexpr (NG == 8)
-        *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
-      else if constexpr (NG == 4)
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-      else if constexpr (NG == 2)
-        w[0] = *reinterpret_cast<const uint16_t*>(p);
-      else
-        w[0] = *p;
-#pragma unroll
-      for (int j = 0; j < NG; ++j) r.z[j] = static_cast<float>(w[j >> 2] >> (8 * (j & 3)) & 15u);
+      if constexpr (NG == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        r.z[0] = v.x, r.z[1] = v.y;
+      } else if constexpr (NG == 4) {
+        r.z[0] = *reinterpret_cast<const uint32_t*>(p);
+      } else if constexpr (NG == 2) {
+        r.z[0] = *reinterpret_cast<const uint16_t*>(p);
+      } else {
+        r.z[0] = *p;
+      }
     }
     return;
   }
+  r = RawGroups<NG>{};
 #pragma unroll
   for (int j = 0; j < NG; ++j)
     if (c * NG + j < groups) {
-      r.s[j] = scale_at(a, at + j);
-      if constexpr (ZERO) r.z[j] = static_cast<float>(a.zero[at + j] & 15u);
+      if (a.sdt == QVLA_DTYPE_F32)
+        r.s[j] = static_cast<const uint32_t*>(a.scale)[at + j];
+      else
+        r.s[j / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(a.scale)[at + j]) << (16 * (j & 1));
+      if constexpr (ZERO) r.z[j / 4] |= static_cast<uint32_t>(a.zero[at + j]) << (8 * (j & 3));
     }
+}
+
+template <int NG, bool ZERO>
+QVLA_DEVICE RowGroups<NG> convert_groups(const GemvArgs& a, const RawGroups<NG>& r) {
+  RowGroups<NG> g = {};
+#pragma unroll
+  for (int j = 0; j < NG; ++j) {
+    if (a.sdt == QVLA_DTYPE_F32)
+      g.s[j] = __uint_as_float(r.s[j]);
+    else
+      g.s[j] = __uint_as_float(j & 1 ? r.s[j / 2] & 0xffff0000u : r.s[j / 2] << 16);
+    if constexpr (ZERO) g.z[j] = static_cast<float>(r.z[j >> 2] >> (8 * (j & 3)) & 15u);
+  }
+  return g;
 }
 
 QVLA_DEVICE void store_y(const GemvArgs& a, int m, int n, float v) {
@@ -486,7 +500,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   pdl_launch_dependents();
   pdl_wait();
   ring.fill(w, codes, lane);
-  RowGroups<NG> next = {};
+  RawGroups<NG> next = {};
   if (w.total) load_groups<NG, ZERO>(a, min(w.band0 * 32 + lane, a.N - 1), w.first, next);
 
   // ---- the byte planes of x: the chunks of this warp's share of K, dealt to
@@ -575,7 +589,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     for (int i = 0; i < w.per_band; ++i) {
       const int c = w.first + i * w.stride, slot = i * sh.WK + w.wk;
       ring.next(w, codes, lane, err);
-      const RowGroups<NG> rg = next;
+      const RowGroups<NG> rg = convert_groups<NG, ZERO>(a, next);
       if (i + 1 < w.per_band)
         load_groups<NG, ZERO>(a, min(band * 32 + lane, a.N - 1), c + w.stride, next);
       else if (band + w.band_step < w.bands)
@@ -772,7 +786,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   ring.fill(w, codes, lane);
   const bool zero = a.zero != nullptr;
   const uint32_t flip = zero ? 0x43004300u : 0x43084308u;
-  RowGroups<NG> next = {};
+  RawGroups<NG> next = {};
   auto load_next = [&](int n, int c) {
     if (zero)
       load_groups<NG, true>(a, min(n, a.N - 1), c, next);
@@ -809,7 +823,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     for (int i = 0; i < w.per_band; ++i) {
       const int c = w.first + i * w.stride;
       ring.next(w, codes, lane, err);
-      const RowGroups<NG> rg = next;
+      const RowGroups<NG> rg = convert_groups<NG, true>(a, next);      // z unused without zero points
       if (i + 1 < w.per_band)
         load_next(band * 32 + lane, c + w.stride);
       else if (band + w.band_step < w.bands)
