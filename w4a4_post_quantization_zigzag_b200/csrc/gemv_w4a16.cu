@@ -823,7 +823,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     for (int i = 0; i < w.per_band; ++i) {
       const int c = w.first + i * w.stride;
       ring.next(w, codes, lane, err);
-      const RowGroups<NG> rg = convert_groups<NG, true>(a, next);      // z unused without zero points
+      const RowGroups<NG> rg = convert_groups<NG, false>(a, next);
+      uint32_t zs[(NG + 3) / 4];
+#pragma unroll
+      for (int j = 0; j < (NG + 3) / 4; ++j) zs[j] = next.z[j];
       if (i + 1 < w.per_band)
         load_next(band * 32 + lane, c + w.stride);
       else if (band + w.band_step < w.bands)
@@ -841,10 +844,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 #pragma unroll
         for (int r = 0; r < 4; ++r) z[r] = 0x43084308u;
         if (zero) {
+          const uint32_t mine = (zs[grp >> 2] >> (8 * (grp & 3)) & 15u) * 0x10001u + 0x43004300u;
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            z[r] = 0x43004300u +
-                   static_cast<uint32_t>(__shfl_sync(0xffffffffu, rg.z[grp], rho + 8 * r)) * 0x10001u;
+          for (int r = 0; r < 4; ++r) z[r] = __shfl_sync(0xffffffffu, mine, rho + 8 * r);
         }
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
