@@ -63,15 +63,16 @@ __global__ void __launch_bounds__(256) pack_w4g_kernel(const float* __restrict__
 // Bound by reading the codes once, so the work per code has to be small.  Two
 // kernels share the way the codes come and how work is dealt; one multiplies
 // in integers and serves one and two activation rows, the other in bf16 and
-// serves more.  (2048 -> 131072, groups of 128: one row 25.6 us in integers,
-// 5.4 TB/s, against 37.7 in bf16, two rows 26.0 against 37.8, three, which
-// would be two passes in integers, 51 against 38; sixteen rows 56.5 us.  1536
-// -> 6144, groups of 32, fp32: one row 6.0 against 7.8 us.  Where the codes
-// fit the SMs at once there is little between them: 4096 -> 4096, one row 5.6
-// against 5.4 us.)  One and two rows of a large matrix are bound by memory
-// (85 % of the copy rate); more rows by the warps' instructions, about 900 per
-// 32 x 256 codes at sixteen rows, half of them to expand the codes; small
-// matrices by the launch and one trip to memory (1024 -> 4096: 3.8 us).
+// serves more.  (2048 -> 131072, groups of 128: one row 24.7 us in integers,
+// 5.7 TB/s, against 34.5 in bf16, two rows 25.0 against 34.8, three, which
+// would be two passes in integers, 51 against 35; sixteen rows 46.8 us, 3.2
+// TB/s.  Groups of 32: one row 49 against 53 us.  Where the codes fit the SMs
+// at once there is little between them: 4096 -> 4096, one row 5.5 against 5.2,
+// two 6.2 against 5.3 us.)  One and two rows of a large matrix are bound by
+// memory (87 % of the copy rate; groups below 128 by the scaling of each group);
+// more rows by the warps' instructions and their latencies, about 820 per 32 x
+// 256 codes at sixteen rows, half of them to expand the codes; small matrices
+// by the launch and one trip to memory (1024 -> 4096: 3.8 us).
 //
 // A warp multiplies bands of 32 weight rows.  A CTA has WR x WK warps: WR
 // groups that take bands in turn, K dealt to the WK warps of a group in chunks
@@ -832,7 +833,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       else if (band + w.band_step < w.bands)
         load_next((band + w.band_step) * 32 + lane, w.first);
       const uint32_t stage = smem_u32(ring.mem) + ring.stage * kStageBytes;
-      // two chains of sums; fp32 x: its first part apart from the rest
+      // fp32 x: its first part's sums apart from the rest's, which the MMA would
+      // cut off (a second chain for bf16 x: 54.1 against 50.2 us at 16 rows)
       float part[XP == 1 ? 1 : 2][2][MT][4];
 #pragma unroll
       for (int seg = 0; seg < kSegs; ++seg) {
@@ -1035,10 +1037,10 @@ template <int G, int MT, int XP>
 cudaError_t run_parts(const GemvArgs& a, GemvShape sh, int sms, cudaStream_t stream) {
   sh.rows = std::min(a.M, 8 * MT);
   // Operand order is worth its staging where warps take several bands
-  // (2048 -> 131072, 16 rows: 56.5 against 67.5 us, 8 rows: 39.2 against 51.9)
-  // or the activations have to be split (1536 -> 6144, seven fp32 rows: 9.6
-  // against 12.2 us), and the activations leave room for rings of two stages.
-  // With one band a warp it changes nothing (4096 -> 4096, 16 rows: 8.2).
+  // (2048 -> 131072, when measured: 16 rows 56.5 against 67.5 us, 8 rows 39.2
+  // against 51.9) or the activations have to be split (1536 -> 6144, seven fp32
+  // rows: 9.6 against 12.2 us), and the activations leave room for rings of two
+  // stages.  With one band a warp it changes nothing (4096 -> 4096, 16 rows).
   GemvShape st = sh;
   if (sh.KC == 1 && (XP > 1 || wanted_ctas(sh, a.N) > sms)) {
     auto bytes = [&](const GemvShape& s) { return part_layout(s, a.K, XP, true).bytes; };
