@@ -22,11 +22,11 @@
 // Each warp feeds itself: cp.async of its own tiles into its own ring of
 // shared memory, no barrier with other warps before the join.
 //
-// One sequence of 131072 tokens, 32 over 8 heads of 128: 93 us, 5.8 TB/s (88 %
+// One sequence of 131072 tokens, 32 over 8 heads of 128: 94 us, 5.7 TB/s (87 %
 // of the copy rate); 32 sequences of up to 8192: 91 us.  With little to read
 // the time is a chain of waits (lengths, page numbers, first tiles, the join,
-// the second launch): 13.6 us at 1040 tokens and 8 over 1 heads of 256, 27.7
-// at 64 sequences that see 2000 tokens in 8 bits (5 us of bytes).
+// the second launch): 12.1 us at 1040 tokens and 8 over 1 heads of 256, 28 at
+// 64 sequences that see 2000 tokens in 8 bits (5 us of bytes).
 #include "qvla_common.cuh"
 #include "qvla_internal.h"
 
@@ -763,44 +763,70 @@ __global__ void __launch_bounds__(32 * W, 1)
       }
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < kHeads * DP / 4; x += 32 * W) {
-      const int h = x / (DP / 4), d = x % (DP / 4) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      int begins = 0;
-#pragma unroll 4
-      for (int k = 0; k < 2 * W; ++k) {
-        if (!(valid >> k & 1)) continue;
+    // A thread's places of the output; the values of four parts, or of four
+    // places of one, asked for at once (one after the other: 13.4 against 12.1
+    // us at 1040 tokens and 8 over 1 heads of 256).
+    constexpr int kPlaces = kHeads * DP / 4, kItems = (kPlaces + 32 * W - 1) / (32 * W);
+    constexpr int kAhead = kItems < 4 ? 4 / kItems : 1;
+    static_assert(kItems == 1 || kPlaces % (32 * W) == 0, "every thread has all its places or none");
+    float4 v[kItems];
+    int begins = 0;
+#pragma unroll 1
+    for (uint32_t rest = static_cast<int>(threadIdx.x) < kPlaces ? valid : 0u; rest;) {
+      float4 p[kAhead][kItems];
+      float w[kAhead][kItems];
+      uint32_t ask = rest;
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b, ask &= ask - 1) {
+        if (!ask) break;
+        const int k = __ffs(ask) - 1;
         const float* src = (k & 1) ? reinterpret_cast<const float*>(ring + (k >> 1) * S * Sh::kStage)
                                    : ws.warp_o + (static_cast<size_t>(blockIdx.x) * W + (k >> 1)) * kHeads * DP;
-        const float4 p = *reinterpret_cast<const float4*>(src + h * DP + d);
-        const float w = slot_weight[k][h];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          const int x = threadIdx.x + i * 32 * W;
+          p[b][i] = *reinterpret_cast<const float4*>(src + x * 4);
+          w[b][i] = slot_weight[k][x / (DP / 4)];
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) {
+        if (!rest) break;
+        const int k = __ffs(rest) - 1;
         if (firsts >> k & 1) {
-          v = make_float4(0.f, 0.f, 0.f, 0.f);
           begins = slot[k].z;
+#pragma unroll
+          for (int i = 0; i < kItems; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (!(w < 0.f)) {
-          v.x += p.x * w;
-          v.y += p.y * w;
-          v.z += p.z * w;
-          v.w += p.w * w;
-        }
-        const uint32_t later = valid & ~(0xffffffffu >> (31 - k));
-        if (later && !(firsts & later & (0u - later))) continue;     // the group goes on
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+          if (!(w[b][i] < 0.f)) {
+            v[i].x += p[b][i].x * w[b][i];
+            v[i].y += p[b][i].y * w[b][i];
+            v[i].z += p[b][i].z * w[b][i];
+            v[i].w += p[b][i].w * w[b][i];
+          }
+        const uint32_t later = rest &= rest - 1;
+        if (later && !(firsts & later & (0u - later))) continue;       // the group goes on
         const int4 u = slot[k];
-        const float2 st = unit_stat[k][h];
-        if (begins && u.w) {
-          const int kh = u.y / HT, hg = u.y % HT * kHeads + h;
-          const float r = st.y == 0.f ? 0.f : 1.f / st.y;
-          if (hg < G && d < D)
-            store_out4<X>(a, u.x, kh * G + hg, d,
-                          st.y == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                      : make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
-          if (d == 0 && a.lse && hg < G) a.lse[static_cast<int64_t>(u.x) * a.Hq + kh * G + hg] = lse_of(st.x, st.y);
-        } else {
-          // its beginning (slot 1) or a later part (slot 0) of a unit that goes on in other CTAs
-          const size_t at = static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0);
-          *reinterpret_cast<float4*>(ws.o + (at * kHeads + h) * DP + d) = v;
-          if (d == 0) ws.stat[at * kSlotHeads + h] = st;
+        const int kh = u.y / HT, h0 = u.y % HT * kHeads;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          const int x = threadIdx.x + i * 32 * W, h = x / (DP / 4), d = x % (DP / 4) * 4, hg = h0 + h;
+          const float2 st = unit_stat[k][h];
+          if (begins && u.w) {
+            const float r = st.y == 0.f ? 0.f : 1.f / st.y;
+            if (hg < G && d < D)
+              store_out4<X>(a, u.x, kh * G + hg, d,
+                            st.y == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                        : make_float4(v[i].x * r, v[i].y * r, v[i].z * r, v[i].w * r));
+            if (d == 0 && a.lse && hg < G) a.lse[static_cast<int64_t>(u.x) * a.Hq + kh * G + hg] = lse_of(st.x, st.y);
+          } else {
+            // its beginning (slot 1) or a later part (slot 0) of a unit that goes on in other CTAs
+            const size_t at = static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0);
+            *reinterpret_cast<float4*>(ws.o + (at * kHeads + h) * DP + d) = v[i];
+            if (d == 0) ws.stat[at * kSlotHeads + h] = st;
+          }
         }
       }
     }
