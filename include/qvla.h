@@ -631,7 +631,8 @@ qvla_status qvla_qk_norm_rope(const void* q, const void* k, const void* v, qvla_
  * and gives o = 0, lse = -inf; a page outside the cache sets it and its
  * tokens are left out.  Cache rows that no visible token owns are not read
  * (they may hold anything).  Products and sums are fp32; for bf16 q the
- * probabilities enter the second product as bf16, for fp32 q whole.  The
+ * probabilities enter the second product in two bf16 parts, which leave out
+ * 2^-15 of each at most, for fp32 q whole.  The
  * split of the work, and with it the order of the sums, depends on all
  * lengths of the call and is the same for equal calls.
  * Asynchronous, two launches.  B <= 2^16, max_pages * page_size <= 2^30.    */

@@ -287,3 +287,21 @@ def test_lse_joins_two_caches(q):
     w = torch.softmax(torch.stack(lses), 0)[..., None]
     _, _, so, _ = R.paged_attn(d["q"], d["kc"], d["vc"], d["tab"], d["lens"], 64 ** -0.5)
     R.within(whole, w[0] * parts[0] + w[1] * parts[1], 3 * so)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq", [8, 20])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_probabilities_lose_nothing_that_shows(q, D, Hq, bits):
+    """bf16 queries: the output takes one rounding of its own, and the probabilities none that is
+    near it, however much the values cancel."""
+    d = setup([2, 3, 5, 17, 200, 1500], Hq, 2, D, bits=bits, seed=D + Hq)
+    if bits == 8:
+        d["vc"].clamp_(min=-127)                       # so that the codes have magnitudes
+    o = run(q, d)
+    args = d["tab"], d["lens"], D ** -0.5, 0, 0, d["ks"], d["vs"]
+    ro, _, so, _ = R.paged_attn(d["q"].float(), d["kc"], d["vc"], *args)
+    mag = R.paged_attn(d["q"].float(), d["kc"], d["vc"].abs(), *args)[0]
+    # so is the bound of fp32 probabilities; cut to 8 bits one leaves less than 2^-7 of itself,
+    # and the bf16 rounding of that is off by 2^-8 of it
+    R.within(o, ro, so + 2.0 ** -15 * mag, "o")
