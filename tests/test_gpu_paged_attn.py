@@ -305,3 +305,37 @@ def test_probabilities_lose_nothing_that_shows(q, D, Hq, bits):
     # so is the bound of fp32 probabilities; cut to 8 bits one leaves less than 2^-7 of itself,
     # and the bf16 rounding of that is off by 2^-8 of it
     R.within(o, ro, so + 2.0 ** -15 * mag, "o")
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 20), (256, 4)])
+def test_infinite_values(q, dt, D, Hq):
+    """A visible infinite value makes its component infinite (of both signs: NaN), also where its
+    token has all the weight, and changes no other."""
+    d = setup([40, 1], Hq, 2, D, dt, junk=False)
+    want, G, inf = run(q, d), Hq // 2, float("inf")
+    p, one = d["tab"][0].long(), d["tab"][1, 0].long()
+    d["vc"][p[1], 3, 0, 7] = d["vc"][p[0], 5, 0, 11] = d["vc"][one, 0, 1, 3] = inf
+    d["vc"][p[0], 2, 0, 9] = d["vc"][p[2], 5, 0, 11] = -inf
+    o = run(q, d)
+    assert (o[0, :G, 7] == inf).all() and (o[0, :G, 9] == -inf).all() and o[0, :G, 11].isnan().all()
+    assert (o[1, G:, 3] == inf).all()
+    o[0, :G, [7, 9, 11]], o[1, G:, 3] = want[0, :G, [7, 9, 11]], want[1, G:, 3]
+    assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 20), (256, 4)])
+def test_infinite_scale_of_a_value(q, dt, D, Hq):
+    """The same in an 8-bit cache: scale times code, NaN where the code is 0."""
+    d = setup([40, 1], Hq, 2, D, dt, bits=8, junk=False)
+    want, G = run(q, d), Hq // 2
+    p, one = d["tab"][0].long(), d["tab"][1, 0].long()
+    d["vc"][p[1], 3, 0, 6] = 0
+    d["vs"][p[1], 3, 0] = d["vs"][one, 0, 1] = float("inf")
+    o = run(q, d)
+    for b, heads, code in ((0, slice(0, G), d["vc"][p[1], 3, 0]), (1, slice(G, Hq), d["vc"][one, 0, 1])):
+        value = (code.float() * float("inf")).to(dt).expand(G, D)
+        assert torch.equal(o[b, heads].isnan(), value.isnan())
+        assert torch.equal(o[b, heads].nan_to_num(7.0), value.nan_to_num(7.0))
+    assert torch.equal(o[0, G:], want[0, G:]) and torch.equal(o[1, :G], want[1, :G])

@@ -649,7 +649,12 @@ __global__ void __launch_bounds__(32 * W, 1)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[k][n][j] += tile[0][n][j] + tile[1][n][j];
+            for (int j = 0; j < 4; ++j) {
+              // an infinite value times a part that is 0 is no number: the first
+              // parts, which are 0 only where p is, have the infinity
+              const float rest = tile[1][n][j];
+              o[k][n][j] += tile[0][n][j] + (rest == rest ? rest : 0.f);
+            }
         }
       };
       constexpr int kStep = BITS == 8 ? 2 : QP == 1 ? 4 : 1;
