@@ -339,3 +339,18 @@ def test_infinite_scale_of_a_value(q, dt, D, Hq):
         assert torch.equal(o[b, heads].isnan(), value.isnan())
         assert torch.equal(o[b, heads].nan_to_num(7.0), value.nan_to_num(7.0))
     assert torch.equal(o[0, G:], want[0, G:]) and torch.equal(o[1, :G], want[1, :G])
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_nan_query_of_any_payload(q, D, bits):
+    """A NaN in an fp32 query makes its head NaN, whichever of its bits say so, and no other head."""
+    d = setup([40, 3], 4, 2, D, F32, bits=bits, junk=False)
+    d["kc"][..., 7] = -1
+    want = run(q, d)
+    for payload in (0x7fc00000, 0x7f800001, 0x7f80ffff, -0x7fffff):          # the last: 0xff800001
+        d["q"][0, 1].view(torch.int32)[7] = payload
+        o = run(q, d)
+        assert o[0, 1].isnan().all()
+        o[0, 1] = want[0, 1]
+        assert torch.equal(o, want)

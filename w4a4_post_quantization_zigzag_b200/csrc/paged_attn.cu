@@ -436,6 +436,9 @@ __global__ void __launch_bounds__(32 * W, 1)
                 v[1] = f0.y;
                 v[2] = f1.x;
                 v[3] = f1.y;
+                // a NaN whose bits are all below its first part would become infinite there
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = v[j] == v[j] ? v[j] : __uint_as_float(0x7fc00000u);
               }
             }
             if constexpr (BITS == 8) {            // even values first, then odd ones
