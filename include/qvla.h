@@ -597,7 +597,9 @@ qvla_status qvla_rope_table(const double* inv_freq, int half, int P, float* tabl
  *           (padding); one past the cache sets QVLA_DEVERR_CACHE_RANGE and
  *           writes nothing.  Slots of one call must differ.  No other byte
  *           of the cache is touched.  bits 8: per row s = max|x| / 127, code
- *           = clamp(rint(x / s), -128, 127), as qvla_rotate_quant_act_a8().
+ *           = clamp(rint(x / s), -128, 127), as qvla_rotate_quant_act_a8();
+ *           a row with an infinite or NaN value gets codes 0 and a NaN scale
+ *           (attention over it is NaN).
  * q_out, k_out    device rows of xdt [T][ldqo], [T][ldko]; may be q and k
  *           themselves (same pitch).  k_out may be NULL.
  * Asynchronous, one launch.                                                 */

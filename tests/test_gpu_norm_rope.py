@@ -264,3 +264,35 @@ def test_graph_replay(q):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(d["kc"], e["kc"]) and torch.equal(d["vc"], e["vc"])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("normed", [True, False])
+def test_non_finite_rows_of_an_8_bit_cache(q, dt, D, normed):
+    """A key or value row with a NaN or an infinity has no 8-bit form: codes 0 and a NaN scale, so
+    that attention over it is NaN as over a bf16 cache; the other rows are what they were."""
+    d = setup(5, 4, 2, D, dt, bits=8, pages=1, seed=D)
+    d["slots"] = torch.arange(5, dtype=torch.int32, device="cuda")
+    if not normed:
+        d["kn"] = None
+    table = q.qvla_rope_table(inv_freq(D), 10)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    e = {k: (v.clone() if torch.is_tensor(v) else v) for k, v in d.items()}
+    nan, inf = float("nan"), float("inf")
+    e["k"][0, 1, 3], e["k"][1, 0, 5], e["k"][2, 0, D - 1] = nan, inf, -inf
+    e["v"][2, 1, 0], e["v"][3, 0, D - 1], e["v"][4, 1, 2] = nan, inf, -inf
+    run(q, d, table, pos)
+    run(q, e, table, pos)
+    for c, s, bad in (("kc", "ks", ((0, 1), (1, 0), (2, 0))), ("vc", "vs", ((2, 1), (3, 0), (4, 1)))):
+        hit = torch.zeros(16, 2, dtype=torch.bool, device="cuda")
+        for t, h in bad:
+            hit[t, h] = True
+        assert torch.equal(e[s][0].isnan(), hit) and (e[c][0][hit] == 0).all()
+        assert torch.equal(e[s][0][~hit], d[s][0][~hit]) and torch.equal(e[c][0][~hit], d[c][0][~hit])
+    x = torch.randn(2, 4, D, device="cuda", generator=gen(1)).to(dt)
+    tab = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([1, 5], dtype=torch.int32, device="cuda")
+    o = q.qvla_paged_attn_decode(x, e["kc"], e["vc"], tab, lens, k_scale=e["ks"], v_scale=e["vs"])
+    assert o[0, :2].isfinite().all() and o[0, 2:].isnan().all() and o[1].isnan().all()
+    assert q.qvla_read_error_word(clear=True) == 0

@@ -49,7 +49,15 @@ QVLA_DEVICE void store8(X* p, const Vec8& r) {
   }
 }
 
-// 8-bit code of x / s, as the 8-bit activation quantiser rounds it.
+// The larger of two magnitudes; NaN if one is.
+QVLA_DEVICE float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 8-bit code of x / s, as the 8-bit activation quantiser rounds it; 0 if s is not
+// above 0 (a row of zeros, or one that has no 8-bit form).
 QVLA_DEVICE uint32_t code8(float x, float s) {
   if (!(s > 0.f)) return 0u;
   return static_cast<uint32_t>(
@@ -226,12 +234,13 @@ QVLA_DEVICE void some_heads(const NormRopeArgs& a, const Lane<X>& ln, int t, int
         float mx = 0.f;
         if (live) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(fabsf(x0.v[j]), fabsf(x1.v[j])));
+          for (int j = 0; j < 8; ++j) mx = max_or_nan(mx, max_or_nan(fabsf(x0.v[j]), fabsf(x1.v[j])));
         }
 #pragma unroll
-        for (int d = LPR / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        for (int d = LPR / 2; d; d >>= 1) mx = max_or_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
         if (live) {
-          const float s = __fdiv_rn(mx, 127.f);
+          // an infinity or a NaN in the row: its scale says so, for no code can
+          const float s = mx < INFINITY ? __fdiv_rn(mx, 127.f) : __uint_as_float(0x7fc00000u);
           int8_t* row = static_cast<int8_t*>(KIND == 1 ? a.cache.k : a.cache.v) + at;
           store_codes(row + ln.c0, x0, s);
           store_codes(row + ln.c1, x1, s);
