@@ -296,3 +296,27 @@ def test_non_finite_rows_of_an_8_bit_cache(q, dt, D, normed):
     o = q.qvla_paged_attn_decode(x, e["kc"], e["vc"], tab, lens, k_scale=e["ks"], v_scale=e["vs"])
     assert o[0, :2].isfinite().all() and o[0, 2:].isnan().all() and o[1].isnan().all()
     assert q.qvla_read_error_word(clear=True) == 0
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("eps", [EPS, 0.0])
+def test_squares_outside_the_range_of_fp32(q, dt, D, eps):
+    """Rows whose squares overflow, and (eps 0) rows whose squares vanish, beside ordinary ones; an
+    infinite row stays NaN."""
+    d = setup(9, 4, 2, D, dt, seed=D)
+    top = torch.finfo(dt).max / 32
+    scale = torch.tensor([1.0, 1e19, 1e22, 1e30, top, 1.0, 1e-19, 1e-25, 1e-30], device="cuda")[:, None, None]
+    for c in "qk":
+        d[c].copy_(d[c].float() * (scale if eps == 0 else scale.clamp(min=1.0)))
+    table = q.qvla_rope_table(inv_freq(D), 10)
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")
+    rows = table[pos.long()]
+    a, b = q.qvla_qk_norm_rope(d["q"], d["k"], None, d["qn"], d["kn"], table, pos, eps=eps)
+    for y, x, w in ((a, d["q"], d["qn"]), (b, d["k"], d["kn"])):
+        R.within(y, *R.norm_rope(x, w, rows[:, :D // 2], rows[:, D // 2:], D, False, eps))
+    d["q"][3, 1, 5] = float("inf")
+    c, _ = q.qvla_qk_norm_rope(d["q"], d["k"], None, d["qn"], d["kn"], table, pos, eps=eps)
+    assert c[3, 1].isnan().any()
+    c[3, 1] = a[3, 1]
+    assert torch.equal(c, a)

@@ -127,6 +127,19 @@ struct Lane {
   int64_t slot_off, scale_off;   // of the token's slot; slot_off < 0: nothing is written
 };
 
+// Mean of the squares of the row that LPR lanes hold.
+template <int LPR>
+QVLA_DEVICE float mean_square(const Vec8& x0, const Vec8& x1, int D) {
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) ss = fmaf(x0.v[j], x0.v[j], fmaf(x1.v[j], x1.v[j], ss));
+#pragma unroll
+  for (int d = LPR / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+  return ss / static_cast<float>(D);
+}
+constexpr uint32_t kLeastMean = 0x0d800000u, kMostMean = 0x71800000u;   // bits of 2^-100 and 2^100
+constexpr float kShrink = 8.07793567e-28f;                              // 2^-90
+
 // Passes [lo, hi) of one kind of head (0 query, 1 key, 2 value) of a token.
 // With norm weight w and r = 1 / sqrt(mean + eps), pairs become
 //   (a, b) -> r (a (w_a c) - b (w_b s)),  r (b (w_b c) + a (w_a s)):
@@ -197,12 +210,21 @@ QVLA_DEVICE void some_heads(const NormRopeArgs& a, const Lane<X>& ln, int t, int
     if constexpr (KIND < 2) {
       float r = 1.f;
       if (w) {
-        float ss = 0.f;
+        float mean = mean_square<LPR>(x0, x1, a.D) + a.eps;
+        // Squares that fp32 does not hold (a row of values past 2^50 or, with no
+        // eps to speak of, below 2^-50, NaN too): once more at another power of two.
+        if (__any_sync(0xffffffffu, __float_as_uint(mean) - kLeastMean > kMostMean - kLeastMean)) {
+          const float by = mean > __uint_as_float(kMostMean)    ? kShrink
+                           : mean < __uint_as_float(kLeastMean) ? 1.f / kShrink
+                                                                : 1.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x0.v[j], x0.v[j], fmaf(x1.v[j], x1.v[j], ss));
-#pragma unroll
-        for (int d = LPR / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        r = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
+          for (int j = 0; j < 8; ++j) {
+            x0.v[j] *= by;
+            x1.v[j] *= by;
+          }
+          mean = mean_square<LPR>(x0, x1, a.D) + a.eps * by * by;
+        }
+        r = rsqrtf(mean);
       }
       if (ln.bad) {
         x0 = x1 = Vec8{};
