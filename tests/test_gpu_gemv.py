@@ -296,3 +296,20 @@ def test_pack(q, group, sdt, zero):
     # rounding to a step, the ends may miss by the rounding of the scale
     assert (err.abs() <= sf[..., None] * (0.5 + 15 * R.half_step(sdt) + (1.0 if zero else 0) * 0.5 + 1e-5)).all()
     check(q, rows(2, K, BF), wq, s, z)
+
+
+@pytest.mark.parametrize("sdt", [F32, BF])
+def test_pack_spans_past_the_largest_float(q, sdt):
+    """Finite weights whose span is not: the scale is, and the codes are the stated ones."""
+    W = torch.zeros(3, 64, device="cuda")
+    W[0, :3] = torch.tensor([-3e38, 3e38, 1e38], device="cuda")
+    W[1, :2] = torch.tensor([-3.4e38, 3.4e38], device="cuda")
+    W[2, :2] = torch.tensor([-1.0, 2.0], device="cuda")
+    wq, s, z = q.qvla_pack_weights_w4g(W, 64, True, sdt)
+    w = W.double()
+    want = ((w.amax(1) - w.amin(1)) / 15).to(sdt)
+    assert torch.equal(s[:, 0], want)
+    sf = want.double()
+    zero = torch.round(-w.amin(1) / sf).clamp(0, 15)
+    assert torch.equal(z[:, 0].double(), zero)
+    assert torch.equal(R.unpack(wq, False), (torch.round(w / sf[:, None]) + zero[:, None]).clamp(0, 15))

@@ -33,7 +33,10 @@ __global__ void __launch_bounds__(256) pack_w4g_kernel(const float* __restrict__
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
   }
-  const float s0 = zero ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(fmaxf(hi, -lo), 7.f);
+  const float span = hi - lo;                  // past the largest float: its half over 7.5
+  const float s0 = !zero            ? __fdiv_rn(fmaxf(hi, -lo), 7.f)
+                   : span < INFINITY ? __fdiv_rn(span, 15.f)
+                                     : __fdiv_rn(0.5f * hi - 0.5f * lo, 7.5f);
   S stored;
   float s;
   if constexpr (sizeof(S) == 2) {
