@@ -531,8 +531,11 @@ qvla_status qvla_pack_weights_w4g(const float* W, int N, int K, int group, qvla_
  * [M][ldy] of ydt (ldx >= K, ldy >= N), apart from x.  Sums are fp32 or
  * wider; y is rounded once.  For one and two rows, each activation enters as
  * an integer multiple of 2^-22 (bf16) or 2^-29 (fp32) of the power of two at
- * or below the largest |x| of its group (an infinite or NaN activation makes
- * its row NaN); for more rows it enters whole (an infinite fp32 one as NaN).
+ * or below the largest |x| of its group (bf16: of 2^-21, where that is in the
+ * last 1/128 below the next power of two), but of 2^-145 at least; an infinite
+ * or NaN activation makes its row NaN.  For more rows it enters whole (fp32:
+ * as a multiple of 2^-133, an infinite one as NaN), and a group's sum has to
+ * be in the range of fp32 before its scale, too.
  * A row's result does not depend on the other rows, nor on M within M <= 2 and
  * within M > 2.  M up to 65535 * 16: the weights are read again for every 16
  * rows, so many rows belong to qvla_w4a4_gemm().  Asynchronous, one launch, no

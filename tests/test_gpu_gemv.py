@@ -313,3 +313,52 @@ def test_pack_spans_past_the_largest_float(q, sdt):
     zero = torch.round(-w.amin(1) / sf).clamp(0, 15)
     assert torch.equal(z[:, 0].double(), zero)
     assert torch.equal(R.unpack(wq, False), (torch.round(w / sf[:, None]) + zero[:, None]).clamp(0, 15))
+
+
+@pytest.mark.parametrize("M", [1, 2, 3])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("zero", [False, True])
+def test_ends_of_the_range_of_activations(q, M, dt, zero):
+    """The largest finite activations, the places where a group's grid changes, and values down to
+    the smallest subnormal, by both kernels."""
+    N, K, G = 48, 256, 64
+    wq, s, z = weights(N, K, G, zero=zero)
+    wq, z = wq & 0x11, z & 1 if zero else None          # codes times values stay in range
+    big, tiny = torch.finfo(dt).max, 2.0 ** (-133 if dt == BF else -149)
+    part = torch.tensor([1.0, 0.77, 0.123456789], device="cuda")[:M]
+    w = R.unpack(wq, False) - (z.double().repeat_interleave(G, 1) if zero else 0)
+    w = (w.view(N, K // G, G) * s.double()[..., None]).abs()
+    for value in (big, 1.9921875 * 2.0 ** 120, 2.0 ** 120, 1.9921875, 1.984375, 2.0, 1.0, 1e-30, 2.0 ** -116, 2.0 ** -117,
+                  2.0 ** -123, 1e-37, 1e-38, 2.0 ** -130, tiny):
+        x = torch.zeros(M, K, dtype=torch.float64, device="cuda")
+        x[:, 5], x[:, 6], x[:, 70] = value * part, value * part / 300, -0.6 * value * part
+        x = x.to(dt)
+        y = q.qvla_w4a16_gemv(x, wq, s, z, out_dtype=F32)
+        ref, slack = R.gemv(x, wq, s, z)
+        # One and two rows: half of the group's grid, 2^-21 (bf16) or 2^-29 of a power of two up
+        # to its largest value, or 2^-145 if that is more.  More rows: an fp32 value is three
+        # values of bf16, whose subnormals are multiples of 2^-133, and loses what is below.
+        # Results below the normal range are off by 2^-150 for each of fewer than 64 operations.
+        top = x.double().abs().view(M, K // G, G).amax(2)
+        grid = (top * 2.0 ** (-21 if dt == BF else -29)).clamp(min=2.0 ** -145)
+        lost = grid / 2 @ w.sum(2).T if M < 3 else (x != 0).double() * 2.0 ** -133 @ w.flatten(1).T * (dt == F32)
+        R.within(y, ref, slack + lost + 2.0 ** -144, f"{value}")
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("N,K,G", [(48, 256, 64), (72, 512, 256), (33, 96, 32)])
+def test_non_finite_row_of_two(q, dt, zero, N, K, G):
+    """One and two rows: an infinity or a NaN makes its row NaN, and the other row is what it is
+    without it."""
+    wq, s, z = weights(N, K, G, zero=zero)
+    x = rows(2, K, dt)
+    clean = q.qvla_w4a16_gemv(x, wq, s, z, out_dtype=F32)
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        for m in (0, 1):
+            for k in (0, 7, K - 1):
+                e = x.clone()
+                e[m, k] = bad
+                y = q.qvla_w4a16_gemv(e, wq, s, z, out_dtype=F32)
+                assert y[m].isnan().all() and torch.equal(y[1 - m], clean[1 - m])
+                assert q.qvla_w4a16_gemv(e[m:m + 1], wq, s, z, out_dtype=F32).isnan().all()

@@ -390,8 +390,12 @@ QVLA_DEVICE void turn_tile(float* tile, const float (&lo)[4], const float (&hi)[
 //
 // What rounding x to its group's grid costs: at most 2^-23 (bf16) or 2^-30
 // (fp32) of the group's largest |x| per element, what an fp32 sum that holds
-// that element may lose with every addition.  bf16 values within 2^14 of the
-// largest, and fp32 values within 2^6, are not rounded at all.
+// that element may lose with every addition; for a bf16 maximum in the last
+// 1/128 below a power of two, whose top byte has to hold 127 and a carry, 1.01
+// times that.  bf16 values within 2^14 of the largest, and fp32 values within
+// 2^6, are not rounded at all.  The grid is never finer than 2^-145 (the factor
+// of the lowest byte is a float), which groups below 2^-123 (bf16) or 2^-116
+// (fp32) meet.
 //
 // The planes are laid out in shared memory once per CTA, while the first codes
 // come.
@@ -676,7 +680,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 
 // ============================================================== three and more
 // The codes become exact bf16 values (u - z) in registers, x enters as bf16
-// (fp32 x as three bf16 parts whose sum is x), every product is exact, a
+// (fp32 x as three bf16 parts whose sum is x, down to 2^-133), every product is exact, a
 // group's sum is fp32 and is scaled once.  The order of K inside an MMA is free
 // as long as both operands agree, so a lane takes the codes as they lie in
 // memory, eight per 32-bit word, and meets them with activations in that order.
