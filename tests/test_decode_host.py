@@ -250,3 +250,29 @@ def test_binding_refuses_host_and_mismatched_tensors(q):
               (h, kc, kc, tab[0], lens), (h.half(), kc, kc, tab, lens)]:
         with pytest.raises((ValueError, TypeError)):
             q.qvla_paged_attn_decode(*a)
+
+
+def test_binding_refuses_every_size_that_32_bits_do_not_hold(q):
+    """Counts of outputs, inputs, positions, heads and head values too."""
+    def meta(*shape, dt=torch.bfloat16):
+        return torch.empty(shape, dtype=dt, device="meta")
+    far, u8, f32 = (1 << 32) + 128, torch.uint8, torch.float32
+    kc, tab = meta(5, 8, 4, 16), meta(1, 3, dt=torch.int32)
+    lens = meta(1, dt=torch.int32)
+    calls = [lambda: q.qvla_w4a16_gemv(meta(1, 32), meta(far, 16, dt=u8), meta(far, 1, dt=f32)),
+             lambda: q.qvla_w4a16_gemv(meta(1, far), meta(4, far // 2, dt=u8), meta(4, far // 128, dt=f32)),
+             lambda: q.qvla_pack_weights_w4g(meta(far, 32, dt=f32), 32),
+             lambda: q.qvla_pack_weights_w4g(meta(1, far, dt=f32), 128),
+             lambda: q.qvla_rope_table(np.ones(1), far, device="meta"),
+             lambda: q.qvla_rope_table(np.ones(1), 1 << 31, device="meta"),
+             lambda: q.qvla_qk_norm_rope(meta(1, far, 16), None),
+             lambda: q.qvla_qk_norm_rope(meta(1, 4, far), None),
+             lambda: q.qvla_qk_norm_rope(None, meta(2, far, 16)),
+             lambda: q.qvla_paged_attn_decode(meta(1, far, 16), kc, kc, tab, lens),
+             lambda: q.qvla_paged_attn_decode(meta(1, 4, 16), meta(5, 8, far, 16), meta(5, 8, far, 16), tab, lens),
+             lambda: q.qvla_paged_attn_decode(meta(1, 4, 16), meta(5, 8, 4, (1 << 32) + 16),
+                                              meta(5, 8, 4, (1 << 32) + 16), tab, lens)]
+    for i, f in enumerate(calls):
+        with pytest.raises(q.QvlaError):
+            f()
+            pytest.fail(f"call {i}")

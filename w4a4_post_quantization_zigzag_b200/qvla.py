@@ -761,6 +761,7 @@ def qvla_pack_weights_w4g(W: torch.Tensor, group: int = 128, zero_points: bool =
     N, K = W.shape
     dev = W.get_device()
     _expect_on(W, torch.float32, (N, K), dev, "W")
+    _expect_int32("W", N | K)
     if group <= 0 or K % group:
         raise QvlaError(QVLA_ERR_SHAPE, "qvla_pack_weights_w4g")
     wq = _empty((N, K // 2), torch.uint8, W.device, stream)
@@ -793,7 +794,7 @@ def qvla_w4a16_gemv(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
         _expect_on(bias, torch.float32, (N,), dev, "bias")
     M = x.shape[0]
     ldx = x.stride(0) if M > 1 else K
-    _expect_int32("x", M | ldx)
+    _expect_int32("x", M | N | K | ldx)
     pitch = (N + 7) // 8 * 8              # rows whose pitch is a multiple of 16 bytes
     if y is None:
         y = _empty((M, pitch), dt, x.device, stream)
@@ -817,6 +818,7 @@ def qvla_rope_table(inv_freq, P: int, device="cuda", stream=None) -> torch.Tenso
     f = np.ascontiguousarray(inv_freq, dtype=np.float64)
     if f.ndim != 1:
         raise ValueError("inv_freq: expected one frequency per pair")
+    _expect_int32("qvla_rope_table", P)
     table = _empty((P, 2 * f.shape[0]), torch.float32, torch.device(device), stream)
     _launch(_lib.qvla_rope_table, "qvla_rope_table", table.get_device(), stream,
             f.ctypes.data_as(c_void_p), f.shape[0], P, table.data_ptr())
@@ -837,10 +839,9 @@ def _head_rows(x: torch.Tensor, shape, device: int, dtype, name: str) -> int:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} rows on cuda:{device} with the "
                          f"heads one after the other, got {x.dtype} {tuple(x.shape)} with strides "
                          f"{tuple(st)} on {x.device}")
-    if shape[0] <= 1:
-        return shape[1] * shape[2]
-    _expect_int32(name, st[0] | shape[0])
-    return st[0]
+    pitch = st[0] if shape[0] > 1 else shape[1] * shape[2]
+    _expect_int32(name, shape[0] | shape[1] | shape[2] | pitch)
+    return pitch
 
 
 def _kv_struct(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale, device: int):
@@ -852,7 +853,7 @@ def _kv_struct(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale, d
                          f"along dim, got shape {tuple(shape)} strides {tuple(st)}")
     if v_cache.shape != shape or v_cache.stride() != st or v_cache.dtype is not dt:
         raise ValueError("v_cache: expected the shape, strides and type of k_cache")
-    _expect_int32("k_cache", shape[0] | shape[1])
+    _expect_int32("k_cache", shape[0] | shape[1] | shape[2] | shape[3])
     if k_cache.get_device() != device or v_cache.get_device() != device:
         raise ValueError(f"k_cache, v_cache: expected them on cuda:{device}")
     if dt is torch.bfloat16:
