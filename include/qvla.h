@@ -637,9 +637,9 @@ qvla_status qvla_qk_norm_rope(const void* q, const void* k, const void* v, qvla_
  * tokens are left out.  Cache rows that no visible token owns are not read
  * (they may hold anything).  Products and sums are fp32; for bf16 q the
  * probabilities enter the second product in two bf16 parts, which leave out
- * 2^-15 of each at most, for fp32 q whole.  The
- * split of the work, and with it the order of the sums, depends on all
- * lengths of the call and is the same for equal calls.
+ * 2^-15 of each at most, for fp32 q whole; one below 2^-126 of its row's
+ * largest counts as 0.  The split of the work, and with it the order of the
+ * sums, depends on all lengths of the call and is the same for equal calls.
  * Asynchronous, two launches.  B <= 2^16, max_pages * page_size <= 2^30.    */
 qvla_status qvla_paged_attn_decode(const void* q, qvla_dtype qdt, int B, int Hq, int ldq,
                                    const qvla_kv_cache* cache, const int32_t* page_table,

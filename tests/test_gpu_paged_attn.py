@@ -354,3 +354,22 @@ def test_nan_query_of_any_payload(q, D, bits):
         assert o[0, 1].isnan().all()
         o[0, 1] = want[0, 1]
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_probabilities_that_vanish(q, dt, bits):
+    """Beside a token that takes all the weight and whose values are 0, the others' share: a
+    probability counts as long as it is 2^-126 of the largest one, or more."""
+    D = 128
+    d = setup([30, 3, 2], 8, 2, D, dt, bits=bits, junk=False)
+    for b in range(3):
+        d["vc"][d["tab"][b, 0].long(), 1] = 0
+        d["kc"][d["tab"][b, 0].long(), 1] = 3
+    d["q"].abs_()
+    for scale in (0.05, 0.2, 0.5, 1.5):
+        o = run(q, d, scale=scale)
+        ro, _, so, _ = R.paged_attn(d["q"], d["kc"], d["vc"], d["tab"], d["lens"], scale, 0, 0, d["ks"], d["vs"])
+        # each of the 30 tokens may lose 2^-126 of its value, twice: cut off, or left in parts
+        most = d["vc"].abs().max().item() if bits == 16 else 128 * d["vs"].max().item()
+        R.within(o, ro, so + 30 * 2.0 ** -125 * most, f"scale {scale}")
