@@ -71,11 +71,15 @@ __global__ void __launch_bounds__(256) pack_w4g_kernel(const float* __restrict__
 // would be two passes in integers, 51 against 35; sixteen rows 46.8 us, 3.2
 // TB/s.  Groups of 32: one row 49 against 53 us.  Where the codes fit the SMs
 // at once there is little between them: 4096 -> 4096, one row 5.5 against 5.2,
-// two 6.2 against 5.3 us.)  One and two rows of a large matrix are bound by
+// two 6.2 against 5.3 us.  fp32 rows of 2048 -> 131072: one 24.8 us, four 48,
+// sixteen 170, in three parts.)  One and two rows of a large matrix are bound by
 // memory (87 % of the copy rate; groups below 128 by the scaling of each group);
 // more rows by the warps' instructions and their latencies, about 820 per 32 x
 // 256 codes at sixteen rows, half of them to expand the codes; small matrices
-// by the launch and one trip to memory (1024 -> 4096: 3.8 us).
+// by the launch and one trip to memory (1024 -> 4096: 3.8 us).  Past sixteen rows
+// every sixteen read and expand all codes again (64 rows of 2048 -> 131072: 188
+// us; 50 of 1024 -> 4096: 10.3).  The kernels of sixteen rows spill at 128
+// registers: bf16 x 4 to 36 bytes, fp32 x up to 108.
 //
 // A warp multiplies bands of 32 weight rows.  A CTA has WR x WK warps: WR
 // groups that take bands in turn, K dealt to the WK warps of a group in chunks

@@ -2,13 +2,15 @@
 //
 //   o = sum_t p_t v_t,  p = softmax over the visible t of scale * q . k_t
 //
-// Bound by reading the cache once: a key head's rows serve all query heads of
+// Bound by reading the cache once: a key head's rows serve the query heads of
 // its group, which are the columns of two small matrix products per 16 tokens,
 //   S^T [16 tokens x heads] = K [16 x D] Q^T [D x heads]
 //   O^T [D x heads]        += V^T [D x 16] P^T [16 x heads]
 // with tokens (then head values) in the rows of the warp-level MMA, so that a
-// group of 8 heads fills its columns.  The running maximum and sum of the
-// softmax are per column; the output stays in registers.
+// group of 8 heads fills its columns.  A larger group has 16 columns (fp32 q at
+// head dims above 128: 8), and one of more heads than that reads the cache once
+// for every 16 (8) of them.  The running maximum and sum of the softmax are per
+// column; the output stays in registers.
 //
 // Work split.  The visible tokens of all sequences and key heads, in tiles of
 // 16, form one line of T tiles that is cut into equal pieces, one per warp of
@@ -22,11 +24,15 @@
 // Each warp feeds itself: cp.async of its own tiles into its own ring of
 // shared memory, no barrier with other warps before the join.
 //
-// One sequence of 131072 tokens, 32 over 8 heads of 128: 94 us, 5.7 TB/s (87 %
-// of the copy rate); 32 sequences of up to 8192: 91 us.  With little to read
-// the time is a chain of waits (lengths, page numbers, first tiles, the join,
-// the second launch): 12.1 us at 1040 tokens and 8 over 1 heads of 256, 28 at
-// 64 sequences that see 2000 tokens in 8 bits (5 us of bytes).
+// One sequence of 131072 tokens, 32 over 8 heads of 128: 93.5 us, 5.7 TB/s (87 %
+// of the copy rate); 32 sequences of up to 8192: 93.4 us (86 %).  With little to
+// read the time is a chain of waits (lengths, page numbers, first tiles, the
+// join, the second launch): 12.5 us at 1040 tokens and 8 over 1 heads of 256.  An
+// 8-bit cache is bound by the instructions that expand its codes: 64 sequences
+// of up to 2000 tokens, 32 over 8 heads of 128, take 55 us in 8 bits and 59 in
+// bf16 (floors of 21 and 41); with fp32 q, in three parts, 62 and 63.  64 that
+// see 2000 tokens of a window in 8 bits, 16 over 2 heads of 64 in fp32: 28.7 us
+// for 5 of bytes, 10 of them instructions.
 #include "qvla_common.cuh"
 #include "qvla_internal.h"
 

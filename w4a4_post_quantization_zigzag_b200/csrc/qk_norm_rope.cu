@@ -281,10 +281,12 @@ QVLA_DEVICE void some_heads(const NormRopeArgs& a, const Lane<X>& ln, int t, int
 
 // CTAs of 256 threads per SM: with three, at 80 registers, the coefficients spill
 // (16381 x 48 heads of 128: 94 against 85 us); rows two or more passes ahead
-// change nothing there (85 to 88 us).
+// change nothing there (85 to 88 us).  With two, bf16 rows spill 4 bytes at most,
+// fp32 rows, twice as wide, 24 to 52.
 constexpr int kResident = 2;
 
-// Bound by reading the rows and writing them back.  A head's row of D values
+// Bound by the rows on the way from memory, of which registers hold too few to
+// fill it (16 KB an SM; DRAM is half busy).  A head's row of D values
 // belongs to LPR = 4, 8 or 16 lanes of a warp; a lane holds two chunks of eight
 // values that hold whole rotation pairs (for separate halves: chunk j and chunk
 // j + rot/16 of the row), so norm, rotation and stores need no exchange but the
@@ -292,8 +294,10 @@ constexpr int kResident = 2;
 // read, so q_out and k_out may be the inputs.  The next pass's rows are loaded
 // before this pass's are worked on.  16381 tokens of 32 + 8 + 8 heads of 128:
 // 85 us for 411 MB read and written, 4.8 TB/s (73 % of the copy rate of large
-// buffers; a plain device copy of 206 MB ran at 3.0).  1024 tokens of 8 + 1 + 1
-// heads of 256: 5.0 us, one token 2.4: the launch and one trip to memory.
+// buffers; a plain device copy of 206 MB ran at 3.0); into an 8-bit cache 114 us,
+// the maximum, divisions and codes of every key and value.  8000 such tokens in
+// fp32: 72 us for 365 MB, 86 into an 8-bit cache.  1024 tokens of 8 + 1 + 1 heads
+// of 256: 5.0 us (8 bits: 7.8), one token 2.5: the launch and one trip to memory.
 template <typename X, int LPR, bool INTER>
 __global__ void __launch_bounds__(256, kResident)
     norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ RowShare sh,
