@@ -160,3 +160,42 @@ def test_bench_decode_workload():
     assert line["value"] > 0 and line["config"]["workload"].startswith("backbone_decode")
     assert line["kernels_per_step"] >= 6 and line["gpu_launches"] == 4 * line["kernels_per_step"]
     assert line["e2e"]["value"] > 0 and line["e2e"]["h2d_bytes_per_step"] == 2048 * 2
+
+
+def test_calls_after_a_failed_one():
+    """The error of a call that cannot run (the error word read inside a capture) belongs to that
+    call alone: each operator's next call runs and says so."""
+    code = '''
+import torch
+from w4a4_post_quantization_zigzag_b200 import qvla as q
+dev, BF = "cuda", torch.bfloat16
+x = torch.randn(3, 256, device=dev).to(BF)
+W = torch.randn(64, 256, device=dev)
+h = torch.randn(2, 4, 64, device=dev).to(BF)
+kc, vc = (torch.randn(4, 16, 2, 64, device=dev).to(BF) for _ in range(2))
+i32 = dict(dtype=torch.int32, device=dev)
+tab, lens = torch.tensor([[0], [1]], **i32), torch.tensor([4, 1], **i32)
+wq, s, z = q.qvla_pack_weights_w4g(W, 64, True)
+calls = [lambda: q.qvla_pack_weights_w4g(W, 64, True)[0], lambda: q.qvla_rope_table([1.0, 0.5], 8),
+         lambda: q.qvla_qk_norm_rope(h, None)[0], lambda: q.qvla_w4a16_gemv(x, wq, s, z),
+         lambda: q.qvla_paged_attn_decode(h, kc, vc, tab, lens)]
+want = [f() for f in calls]
+torch.cuda.synchronize()
+for f, w in zip(calls, want):
+    failed = 0
+    try:
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            try:
+                q.qvla_read_error_word()
+            except q.QvlaError:
+                failed += 1
+    except RuntimeError:
+        failed += 1
+    assert failed == 2
+    got = f()
+    torch.cuda.synchronize()
+    assert torch.equal(got, w)
+assert q.qvla_read_error_word() == 0
+'''
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -1087,13 +1087,15 @@ cudaError_t run_group(const GemvArgs& a, cudaStream_t stream) {
 cudaError_t launch_pack_w4g(const float* W, int N, int K, int group, qvla_dtype sdt, uint8_t* wq,
                             void* scale, uint8_t* zero, cudaStream_t s) {
   const int64_t groups = static_cast<int64_t>(N) * (K / group);
-  const unsigned grid = static_cast<unsigned>((groups + 7) / 8);
+  // a launch that returns its own status, not an error that an earlier call left
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((groups + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
   if (sdt == QVLA_DTYPE_F32)
-    pack_w4g_kernel<<<grid, 256, 0, s>>>(W, groups, group, wq, static_cast<float*>(scale), zero);
-  else
-    pack_w4g_kernel<<<grid, 256, 0, s>>>(W, groups, group, wq, static_cast<__nv_bfloat16*>(scale),
-                                         zero);
-  return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, pack_w4g_kernel<float>, W, groups, group, wq, static_cast<float*>(scale), zero);
+  return cudaLaunchKernelEx(&cfg, pack_w4g_kernel<__nv_bfloat16>, W, groups, group, wq,
+                            static_cast<__nv_bfloat16*>(scale), zero);
 }
 
 cudaError_t launch_w4a16_gemv(const GemvArgs& a, cudaStream_t stream) {

@@ -378,8 +378,12 @@ cudaError_t launch_typed(const NormRopeArgs& a, cudaStream_t stream) {
 cudaError_t launch_rope_table(const RopeFreqs& freqs, int half, int P, float* table,
                               cudaStream_t s) {
   const int64_t total = static_cast<int64_t>(P) * half;
-  rope_table_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, s>>>(freqs, half, total, table);
-  return cudaGetLastError();
+  // a launch that returns its own status, not an error that an earlier call left
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((total + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, rope_table_kernel, freqs, half, total, table);
 }
 
 cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
